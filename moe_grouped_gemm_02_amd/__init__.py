@@ -553,3 +553,8 @@ def dg_describe_config(layout, m, n, k, num_groups=1, num_cus=256, expected_m=0)
 def raw():
     """The loaded ctypes library (for calling entry points with raw pointers)."""
     return _lib
+
+
+# The operators around the grouped GEMMs in a mixture-of-experts layer
+# (include/dg_moe.h): routing, the token exchange, 8-bit checkpoints.
+from .moe import *  # noqa: E402,F401,F403

@@ -34,7 +34,8 @@ ASAN_LIB = os.path.join(HERE, "libdg_host_asan.so")
 # benchmark loads; the GEMM library does not contain it.
 PROBE_LIB = os.path.join(HERE, "libdg_probe.so")
 PROBE_SOURCES = ["dg_probe.hip"]
-SOURCES = ["dg_api.hip", "dg_quant.hip", "dg_gemm.hip"]
+SOURCES = ["dg_api.hip", "dg_quant.hip", "dg_gemm.hip",
+           "dg_moe_api.hip", "dg_route.hip", "dg_exchange.hip", "dg_ckpt.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

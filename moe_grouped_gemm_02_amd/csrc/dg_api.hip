@@ -13,11 +13,13 @@
 
 #include "dg.h"
 #include "dg_internal.h"
+#include "dg_status.h"
 
 namespace {
-
 thread_local char g_last_error[512] = "";
-std::atomic<int> g_num_cus_override{0};
+}  // namespace
+
+namespace dg {
 
 int fail(int status, const char* fmt, ...) {
   va_list ap;
@@ -32,14 +34,16 @@ int ok() {
   return DG_SUCCESS;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace dg
 
-// count * stride * elem < lim, for count, stride >= 0 and elem, lim > 0,
-// decided without forming the product (strides come from the caller).
-bool below(int64_t count, int64_t stride, int64_t elem, int64_t lim) {
-  if (count == 0 || stride == 0) return true;
-  return stride <= (lim - 1) / elem / count;
-}
+namespace {
+
+using dg::aligned16;
+using dg::below;
+using dg::fail;
+using dg::ok;
+
+std::atomic<int> g_num_cus_override{0};
 
 int env_num_cus() {
   const char* s = getenv("DG_NUM_CUS");

@@ -1,0 +1,317 @@
+// Exchange between token rows and expert rows for gfx950: the row plan (a
+// stable counting sort of the routed entries by expert), the dispatch into
+// quantised expert rows, the weighted combine and its gradient.
+
+#include "dg_device.h"
+#include "dg_moe_internal.h"
+#include "dg_tile.h"
+
+namespace dg {
+namespace {
+
+// ------------------------------------------------------------------- plan --
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+
+// Local expert of an entry, or -1.
+__device__ __forceinline__ int local_of(int id, const PlanParams& p) {
+  const int64_t g = (int64_t)id - p.first;
+  return g >= 0 && g < p.groups && id >= 0 ? (int)g : -1;
+}
+
+// Counts the experts of each block's 1024 entries.
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) {
+  __shared__ int count[kMaxLocalExperts];
+  for (int g = threadIdx.x; g < p.groups; g += kPlanThreads) count[g] = 0;
+  __syncthreads();
+  const int64_t i = (int64_t)blockIdx.x * kPlanThreads + threadIdx.x;
+  const int g = i < p.entries ? local_of(p.ids[i], p) : -1;
+  if (g >= 0) atomicAdd(&count[g], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.groups; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.groups + e] = count[e];
+}
+
+// Places each block's 1024 entries and fills the index arrays of its share of
+// the layout's rows.
+__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) {
+  __shared__ int start[kMaxLocalExperts + 1];  // first row of each group
+  __shared__ int count[kMaxLocalExperts];      // entries of each group
+  __shared__ int base[kMaxLocalExperts];       // entries of each group before this block
+  __shared__ uint16_t per_wave[kPlanWaves][kMaxLocalExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int g = tid; g < p.groups; g += kPlanThreads) {
+    int before = 0, all = 0;
+    for (int b = 0; b < (int)gridDim.x; ++b) {
+      if (b == (int)blockIdx.x) before = all;
+      all += p.hist[(int64_t)b * p.groups + g];
+    }
+    count[g] = all;
+    base[g] = before;
+  }
+  for (int i = tid; i < kPlanWaves * p.groups; i += kPlanThreads) per_wave[i / p.groups][i % p.groups] = 0;
+  __syncthreads();
+  if (tid == 0) {
+    int64_t at = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      start[g] = (int)(at < p.layout_rows ? at : p.layout_rows);
+      at += p.masked ? p.m_max : ((int64_t)count[g] + kBlockK - 1) / kBlockK * kBlockK;
+    }
+    start[p.groups] = (int)(at < p.layout_rows ? at : p.layout_rows);
+  }
+
+  const int64_t i = (int64_t)blockIdx.x * kPlanThreads + tid;
+  const int g = i < p.entries ? local_of(p.ids[i], p) : -1;
+  // Lanes of this wave with the same expert.
+  uint64_t same = __ballot(g >= 0);
+  for (int bit = 1; bit < p.groups; bit <<= 1) {
+    const uint64_t ones = __ballot(g & bit);
+    same &= (g & bit) ? ones : ~ones;
+  }
+  const int ahead = __popcll(same & ((1ull << lane) - 1ull));
+  if (g >= 0 && ahead == 0) per_wave[wave][g] = (uint16_t)__popcll(same);
+  __syncthreads();
+  if (i < p.entries) {
+    int row = -1;
+    if (g >= 0) {
+      int rank = base[g] + ahead;
+      for (int w = 0; w < wave; ++w) rank += per_wave[w][g];
+      const int64_t at = (int64_t)start[g] + rank;
+      const int64_t end = p.masked ? (int64_t)start[g] + p.m_max : p.layout_rows;
+      if (at < end) {
+        row = (int)at;
+        p.src[row] = (int)i;
+      }
+    }
+    p.rows[i] = row;
+  }
+
+  const int64_t all_threads = (int64_t)gridDim.x * kPlanThreads;
+  for (int64_t r = i; r < p.layout_rows; r += all_threads) {
+    int lo = 0, hi = p.groups;  // the last group that starts at or before row r and holds rows
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (start[mid] <= r) lo = mid;
+      else hi = mid;
+    }
+    const bool used = r - start[lo] < count[lo];
+    if (!used) p.src[r] = -1;
+    if (p.m_indices) p.m_indices[r] = used ? lo : -1;
+  }
+  if (blockIdx.x == 0) {
+    for (int e = tid; e <= p.groups; e += kPlanThreads) {
+      if (p.k_offsets) p.k_offsets[e] = start[e];
+      if (p.masked_m && e < p.groups) p.masked_m[e] = count[e] < p.m_max ? count[e] : p.m_max;
+    }
+  }
+}
+
+// --------------------------------------------------------------- dispatch --
+
+// Row-wise gather and quantise, the mapping of the plain activation
+// quantiser: 8 lanes own a 128-value tile, a wave owns 8 tiles of a row and
+// U rows at a time.
+constexpr int kTilesPerWave = 8;
+constexpr int kRowWaves = 4;
+
+template <bool POW2, int U>
+__global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams p) {
+  const int tiles_per_row = p.cols / kBlockK;
+  const int64_t total_rows = (int64_t)p.groups * p.rows;
+  const int64_t entries = (int64_t)p.tokens * p.topk;
+  const int sub = threadIdx.x & 7;
+  const int j = blockIdx.x * kTilesPerWave + ((threadIdx.x & 63) >> 3);
+  const int wave = threadIdx.x >> 6;
+  if (j >= tiles_per_row) return;
+  const int64_t step = (int64_t)gridDim.y * kRowWaves * U;
+  for (int64_t r0 = ((int64_t)blockIdx.y * kRowWaves + wave) * U; r0 < total_rows; r0 += step) {
+    uint4 lo[U], hi[U];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = r0 + u < total_rows ? p.src[r0 + u] : -1;
+      live[u] = e >= 0 && e < entries;
+      lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+      if (live[u]) {
+        const uint16_t* from = p.x + (int64_t)(e / p.topk) * p.ld_x + j * kBlockK + sub * 16;
+        lo[u] = *reinterpret_cast<const uint4*>(from);
+        hi[u] = *reinterpret_cast<const uint4*>(from + 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!live[u]) continue;
+      const int64_t gr = r0 + u;
+      const int64_t g = gr / p.rows, r = gr - g * p.rows;
+      const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[i] & 0xFFFFu)), fabsf(bf16_bits_to_f32(w[i] >> 16))));
+#pragma unroll
+      for (int off = 4; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 8));
+      uint32_t out[4];
+      const int64_t sf_at = (g * tiles_per_row + j) * p.ld_sf + r;
+      if constexpr (POW2) {
+        const uint32_t e = ue8m0_exponent(amax);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          out[i] = e4m3_x4(pow2_quotient(w[2 * i] & 0xFFFFu, e), pow2_quotient(w[2 * i] >> 16, e),
+                           pow2_quotient(w[2 * i + 1] & 0xFFFFu, e), pow2_quotient(w[2 * i + 1] >> 16, e));
+        if (sub == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
+      } else {
+        const float s = amax / 448.0f;
+        const double rcp = tile_reciprocal(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          out[i] = e4m3_x4(quotient(w[2 * i] & 0xFFFFu, rcp), quotient(w[2 * i] >> 16, rcp),
+                           quotient(w[2 * i + 1] & 0xFFFFu, rcp), quotient(w[2 * i + 1] >> 16, rcp));
+        if (sub == 0) static_cast<float*>(p.sf)[sf_at] = s;
+      }
+      *reinterpret_cast<uint4*>(p.q + gr * p.cols + j * kBlockK + sub * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- combine --
+
+// Workgroup (x, t): 2048 columns of token t, 8 a thread.
+constexpr int kCombineThreads = 256;
+
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams p) {
+  const int64_t t = blockIdx.x;
+  const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
+  if (col >= p.cols) return;
+  float acc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+  for (int j = 0; j < p.topk; ++j) {
+    const int r = p.rows[t * p.topk + j];
+    if (r < 0 || r >= p.total_rows) continue;
+    const float w = p.weights ? p.weights[t * p.topk + j] : 1.0f;
+    const uint4 v = *reinterpret_cast<const uint4*>(p.d + (int64_t)r * p.ld_d + col);
+    const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      acc[2 * c] = fmaf(w, bf16_bits_to_f32(b[c] & 0xFFFFu), acc[2 * c]);
+      acc[2 * c + 1] = fmaf(w, bf16_bits_to_f32(b[c] >> 16), acc[2 * c + 1]);
+    }
+  }
+  auto bf = [](float f) { return f == f ? f32_to_bf16_rne(f) : 0x7FC0u; };
+  uint32_t o[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) o[c] = bf(acc[2 * c]) | (bf(acc[2 * c + 1]) << 16);
+  *reinterpret_cast<uint4*>(p.y + t * p.ld_y + col) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Workgroup (x, y): rows [128 x, 128 x + 128), columns [128 y, 128 y + 128).
+__global__ __launch_bounds__(kTileThreads) void combine_bwd_kernel(CombineBwdParams p) {
+  __shared__ TileLds lds;
+  const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
+  const int col0 = blockIdx.y * kBlockK;
+  const int tid = threadIdx.x, r0 = (tid >> 4) * 4, c0 = (tid & 15) * 8;
+  const int64_t entries = (int64_t)p.tokens * p.topk;
+  float v[4][8];
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = row0 + r0 + i;
+    const int e = p.src[r];
+    const bool used = e >= 0 && e < entries;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    float w = 0.0f;
+    if (used) {
+      live |= 1u << i;
+      a = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / p.topk) * p.ld_dy + col0 + c0);
+      b = *reinterpret_cast<const uint4*>(p.d + r * p.ld_d + col0 + c0);
+      w = p.weights[e];
+    }
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float x0 = bf16_bits_to_f32(x[c] & 0xFFFFu), x1 = bf16_bits_to_f32(x[c] >> 16);
+      dot = fmaf(x0, bf16_bits_to_f32(y[c] & 0xFFFFu), dot);
+      dot = fmaf(x1, bf16_bits_to_f32(y[c] >> 16), dot);
+      v[i][2 * c] = w * x0;
+      v[i][2 * c + 1] = w * x1;
+    }
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 16);
+    if (used && c0 == 0) p.dots[r * (p.cols / kBlockK) + blockIdx.y] = dot;
+  }
+  tile_rows(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + blockIdx.y * p.ld_dsf + row0, live);
+  if (!p.dqt) return;
+  if (!__syncthreads_or(live != 0)) return;
+  tile_columns(v, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total,
+               p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0);
+}
+
+// dweights of each entry: 16 lanes add the dot products of its row's tiles.
+__global__ __launch_bounds__(256) void combine_dweights_kernel(CombineBwdParams p) {
+  const int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t entries = (int64_t)p.tokens * p.topk;
+  if (i >= entries) return;
+  const int r = p.rows[i], tiles = p.cols / kBlockK, sub = threadIdx.x & 15;
+  float sum = 0.0f;
+  if (r >= 0 && r < p.m_total && p.src[r] == i)
+    for (int j = sub; j < tiles; j += 16) sum += p.dots[(int64_t)r * tiles + j];
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 16);
+  if (sub == 0) p.dweights[i] = sum;
+}
+
+int plan_blocks(int64_t entries) {
+  const int64_t b = (entries + kPlanThreads - 1) / kPlanThreads;
+  return (int)(b > 0 ? b : 1);
+}
+
+}  // namespace
+
+size_t plan_workspace_bytes(int64_t entries, int groups) {
+  return (size_t)plan_blocks(entries) * groups * sizeof(int32_t);
+}
+
+hipError_t launch_plan(const PlanParams& p, hipStream_t stream) {
+  const dim3 grid(plan_blocks(p.entries)), block(kPlanThreads);
+  hipLaunchKernelGGL(plan_count_kernel, grid, block, 0, stream, p);
+  hipLaunchKernelGGL(plan_place_kernel, grid, block, 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t stream) {
+  const int gx = (p.cols / kBlockK + kTilesPerWave - 1) / kTilesPerWave;
+  const int64_t total = (int64_t)p.groups * p.rows;
+  const int u = total >= 16384 ? 4 : total >= 2048 ? 2 : 1;
+  int64_t gy = (16384 / kRowWaves + gx - 1) / gx;
+  const int64_t need = (total + kRowWaves * u - 1) / (kRowWaves * u);
+  if (gy > need) gy = need;
+  const dim3 grid(gx, (unsigned)(gy < 1 ? 1 : gy > 65535 ? 65535 : gy)), block(64 * kRowWaves);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
+  if (pow2) {
+    if (u == 4) go(dispatch_kernel<true, 4>);
+    else if (u == 2) go(dispatch_kernel<true, 2>);
+    else go(dispatch_kernel<true, 1>);
+  } else {
+    if (u == 4) go(dispatch_kernel<false, 4>);
+    else if (u == 2) go(dispatch_kernel<false, 2>);
+    else go(dispatch_kernel<false, 1>);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
+  const dim3 grid(p.tokens, (p.cols / 8 + kCombineThreads - 1) / kCombineThreads);
+  hipLaunchKernelGGL(combine_kernel, grid, dim3(kCombineThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream) {
+  if (p.m_total > 0)
+    hipLaunchKernelGGL(combine_bwd_kernel, dim3(p.m_total / kBlockK, p.cols / kBlockK), dim3(kTileThreads), 0, stream, p);
+  const int64_t entries = (int64_t)p.tokens * p.topk;
+  hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)((entries + 15) / 16)), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace dg

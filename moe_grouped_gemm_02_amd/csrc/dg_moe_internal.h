@@ -1,0 +1,125 @@
+// Internal host/device interface of the mixture-of-experts operators
+// (dg_moe.h): what dg_moe_api.hip has checked and the kernels rely on.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dg {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 32;
+constexpr int kMaxExpertGroups = 64;
+constexpr int kMaxLocalExperts = 1024;
+
+struct RouteParams {
+  const void* logits;  // [tokens][ld], fp32 or bf16
+  const float* bias;   // null: none
+  int32_t* ids;        // backward: read
+  float* weights;
+  const float* dweights;
+  void* dlogits;
+  int tokens, experts, topk;
+  int64_t ld, ld_d;
+  int sigmoid;  // 0: softmax
+  int groups, topk_groups, group_top;
+  int renormalize;
+  float scale;
+};
+hipError_t launch_route(const RouteParams& p, bool bf16, hipStream_t stream);
+hipError_t launch_route_bwd(const RouteParams& p, bool bf16, hipStream_t stream);
+
+struct PlanParams {
+  const int32_t* ids;
+  int32_t* rows;
+  int32_t* src;
+  int32_t* m_indices;  // contiguous only
+  int32_t* k_offsets;  // contiguous only
+  int32_t* masked_m;   // masked only
+  int32_t* hist;       // [blocks][groups], null when one block does it all
+  int entries;         // tokens * topk
+  int first, groups;
+  int masked, m_max;   // masked layout and its rows per group
+  int layout_rows;
+};
+size_t plan_workspace_bytes(int64_t entries, int groups);
+hipError_t launch_plan(const PlanParams& p, hipStream_t stream);
+
+struct DispatchParams {
+  const uint16_t* x;
+  const int32_t* src;
+  uint8_t* q;
+  void* sf;
+  int tokens, topk, cols, rows, groups;
+  int64_t ld_x, ld_sf;
+};
+hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t stream);
+
+struct CombineParams {
+  const uint16_t* d;
+  const int32_t* rows;
+  const float* weights;  // null: ones
+  uint16_t* y;
+  int tokens, topk, cols, total_rows;
+  int64_t ld_d, ld_y;
+};
+hipError_t launch_combine(const CombineParams& p, hipStream_t stream);
+
+struct CombineBwdParams {
+  const uint16_t* dy;
+  const uint16_t* d;
+  const int32_t* src;
+  const int32_t* rows;
+  const float* weights;
+  uint8_t* dq;
+  float* dsf;
+  uint8_t* dqt;  // null: no transposed codes
+  float* dsft;
+  float* dweights;
+  float* dots;  // [m_total][cols / 128] partial sums of the weights' gradient
+  int tokens, topk, cols, m_total;
+  int64_t ld_dy, ld_d, ld_dsf, ld_dsft;
+};
+hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream);
+
+struct SwigluParams {
+  const uint16_t* h;
+  const int32_t* m_indices;  // at most one of the two is given
+  const int32_t* masked_m;
+  uint8_t* q;
+  void* sf;
+  uint8_t* hq;  // null: no checkpoint
+  float* hsf;
+  int rows, inter, groups;
+  int64_t ld_h, ld_sf, ld_hsf;
+};
+hipError_t launch_swiglu_quant(const SwigluParams& p, bool pow2, hipStream_t stream);
+
+struct SwigluBwdParams {
+  const uint8_t* hq;
+  const float* hsf;
+  const uint16_t* dact;
+  const int32_t* m_indices;  // null: every row in use
+  uint8_t* dq;
+  float* dsf;
+  uint8_t* dqt;
+  float* dsft;
+  uint8_t* aqt;  // null: not wanted
+  float* asft;
+  int m_total, inter;
+  int64_t ld_hsf, ld_dact, ld_dsf, ld_dsft, ld_asft;
+};
+hipError_t launch_swiglu_bwd(const SwigluBwdParams& p, hipStream_t stream);
+
+struct RequantParams {
+  const uint8_t* q;
+  const float* sf;
+  const int32_t* m_indices;
+  uint8_t* qt;
+  float* sft;
+  int rows, cols;
+  int64_t ld_sf, ld_sft;
+};
+hipError_t launch_requant_t(const RequantParams& p, hipStream_t stream);
+
+}  // namespace dg

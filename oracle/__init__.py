@@ -19,6 +19,8 @@ majors    the dense GEMM with the NN, TN and TT operand majors and the 1x128
           quantiser of an M-major (column-stored) activation matrix.
 kgrouped  the K-axis grouped GEMM (groups of 128-aligned K ranges, 1x128
           scales along K on both operands) and its exact brute force.
+moe       the operators around the GEMMs in a mixture-of-experts layer: routing,
+          the row plan, combine, the gated unit, and their gradients, in fp64.
 bf16      bit-level helpers for bf16 storage and RNE rounding to bf16.
 
 Sources (the method is described on public pages about DeepSeek's DeepGEMM):
@@ -41,4 +43,4 @@ tests/test_oracle_*.py against things other than itself (torch's CPU e4m3
 cast, exact rational brute force, closed forms, invariants).
 """
 
-from . import bf16, e4m3, gemm, kgrouped, majors, quant, ue8m0  # noqa: F401
+from . import bf16, e4m3, gemm, kgrouped, majors, moe, quant, ue8m0  # noqa: F401
