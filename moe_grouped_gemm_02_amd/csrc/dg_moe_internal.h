@@ -23,6 +23,7 @@ struct RouteParams {
   int64_t ld, ld_d;
   int sigmoid;  // 0: softmax
   int groups, topk_groups, group_top;
+  int per_group, group_shift;  // experts of a group; log2 of its lanes, or -1 (set by the launch)
   int renormalize;
   float scale;
 };

@@ -1,11 +1,14 @@
 // Expert routing for gfx950: scores, grouped top-k and weights, and the
 // gradient of the weights with respect to the logits.
 //
-// One wave holds one token: expert e sits in lane e % 64, register e / 64, so
-// a load of 64 consecutive logits is coalesced for any row stride and any
-// number of experts, and every reduction stays inside the wave.
+// One wave holds one token, lane l experts V l .. V l + V - 1 with V the power
+// of two that covers all experts, so that a row is one vector load a lane, the
+// order of lanes and registers is the order of the experts (ties), and every
+// reduction stays in registers (row operations and readlane, no shared memory).
+// A token is read once; what bounds the kernels is the issue of vector
+// instructions, about 250 a token of 256 experts.
 
-#include "dg_device.h"
+#include "dg_math.h"
 #include "dg_moe_internal.h"
 
 namespace dg {
@@ -13,228 +16,278 @@ namespace {
 
 constexpr int kWaves = 4;  // tokens of a workgroup
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(uint16_t* p, float v) {
-  *p = (uint16_t)(v == v ? f32_to_bf16_rne(v) : 0x7FC0u);
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return bf16_bits_to_f32(v); }
+__device__ __forceinline__ void narrow(float& to, float v) { to = v; }
+__device__ __forceinline__ void narrow(uint16_t& to, float v) {
+  to = (uint16_t)(v == v ? f32_to_bf16_rne(v) : 0x7FC0u);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
+// V consecutive elements as one access of up to 16 bytes.
+template <typename T, int V>
+struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+  T v[V];
+};
+
+// The lane's V logits, -inf past the last expert.  VEC: rows and their length
+// allow whole vectors (decided on the host).
+template <bool VEC, typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int experts, int lane, float (&x)[V]) {
+  const int e0 = lane * V;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
+    for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+    if (e0 < experts) {
+      const Pack<T, V> in = *reinterpret_cast<const Pack<T, V>*>(row + e0);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+      for (int i = 0; i < V; ++i) x[i] = widen(in.v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = e0 + i < experts ? widen(row[e0 + i]) : -INFINITY;
+  }
 }
 
-// Order of a float as an unsigned number: larger value, larger number, -0
-// like +0; 0 for values that are never chosen (-inf and NaN).
-__device__ __forceinline__ uint32_t order_of(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  const uint32_t o = (u >> 31) ? ~u : (u | 0x80000000u);
-  return v > -INFINITY ? o : 0u;
-}
-
-// Scores of the wave's token: lane l holds experts l + 64 i.
+// Scores of the wave's token.
 template <int V>
-__device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], int experts, int lane, bool sigmoid) {
-  if (sigmoid) {
+__device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], bool sigmoid_scores) {
+  if (sigmoid_scores) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = 1.0f / (1.0f + expf(-x[i]));
+    for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]).sig;
     return;
   }
-  float top = -INFINITY;
+  uint32_t most = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
-  top = wave_max(top);
-  if (top == -INFINITY) top = 0.0f;  // nothing but masked experts: every score is 0
+  for (int i = 0; i < V; ++i) most = umax(most, order_of(x[i]));
+  most = wave_max(most);
+  const float top = most ? of_order(most) : 0.0f;  // nothing but masked experts: every score is 0
   float total = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    s[i] = lane + 64 * i < experts ? expf(x[i] - top) : 0.0f;
+    const float d = x[i] - top;
+    const float e = exp_to_80(d);
+    s[i] = d == d ? e : d;
     total += s[i];
   }
   total = wave_sum(total);
-  if (total == 0.0f) total = 1.0f;
+  const float inv = total == 0.0f ? 0.0f : reciprocal(total);
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[i] /= total;
+  for (int i = 0; i < V; ++i) s[i] *= inv;
 }
 
-template <typename T, int V>
+// The two largest of two sorted pairs.
+__device__ __forceinline__ void merge_top2(uint32_t& a, uint32_t& b, uint32_t a2, uint32_t b2) {
+  b = umax(umin(a, a2), umax(b, b2));
+  a = umax(a, a2);
+}
+
+// BIAS, GROUPS: whether the call has them.
+template <bool VEC, typename T, int V, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
-  __shared__ float keys[kWaves][64 * V];
-  __shared__ uint32_t gkeys[kWaves][kMaxExpertGroups];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float lds[kWaves][64 * V];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= p.tokens) return;
-  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float x[V], s[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < p.experts ? load_logit(row + e) : -INFINITY;
-  }
-  scores<V>(x, s, p.experts, lane, p.sigmoid != 0);
-
+  float x[V], s[V], bias[V];
   uint32_t key[V];  // 0: cannot be chosen
+  int idx[V];
+  load_row<VEC>(static_cast<const T*>(p.logits) + t * p.ld, p.experts, lane, x);
+  if constexpr (BIAS) load_row<VEC>(p.bias, p.experts, lane, bias);
+  scores<V>(x, s, p.sigmoid != 0);
+#pragma unroll
+  for (int i = 0; i < V; ++i) lds[wave][lane * V + i] = s[i];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    const float biased = p.bias && e < p.experts ? s[i] + p.bias[e] : s[i];
-    key[i] = x[i] > -INFINITY ? order_of(p.bias ? biased : x[i]) : 0u;
-    if (p.groups > 1) keys[wave][e] = x[i] > -INFINITY ? biased : -INFINITY;
+    if constexpr (BIAS) s[i] += bias[i];
+    const uint32_t k = order_of(BIAS || GROUPS ? s[i] : x[i]);
+    key[i] = (!BIAS && !GROUPS) || x[i] > -INFINITY ? k : 0u;
+    idx[i] = i;
   }
 
-  if (p.groups > 1) {
-    // Lane g scores group g; a group stays where fewer than topk_groups others
-    // come before it.
-    const int per = p.experts / p.groups;
-    __builtin_amdgcn_wave_barrier();
-    uint32_t mine = 0;
-    if (lane < p.groups) {
-      float a = -INFINITY, b = -INFINITY;
-      for (int i = 0; i < per; ++i) {
-        const float v = keys[wave][lane * per + i];
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
-      }
-      if (p.group_top == 2 && b > -INFINITY) a += b;
-      mine = order_of(a);
-      gkeys[wave][lane] = mine;
+  if constexpr (GROUPS) {
+    // Two largest keys of each group: in groups of 2^n whole lanes by row
+    // operations, otherwise lane g walks group g in shared memory (256 experts in
+    // 8 groups, 32768 tokens: the walk costs 22 us more).
+    uint32_t a = 0, b = 0;
+    const bool whole = p.group_shift >= 0;
+    const int mine = whole ? lane >> p.group_shift : lane;  // the group this lane holds the score of
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) merge_top2(a, b, key[i], 0u);
+      if (p.group_shift > 0) merge_top2(a, b, dpp<kXor1>(a), dpp<kXor1>(b));
+      if (p.group_shift > 1) merge_top2(a, b, dpp<kXor2>(a), dpp<kXor2>(b));
+      if (p.group_shift > 2) merge_top2(a, b, dpp<kHalfMirror>(a), dpp<kHalfMirror>(b));
+      if (p.group_shift > 3) merge_top2(a, b, dpp<kRowMirror>(a), dpp<kRowMirror>(b));
+      if (p.group_shift > 4) merge_top2(a, b, __shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
+    } else {
+      __shared__ uint32_t keys[kWaves][64 * V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) keys[wave][lane * V + i] = key[i];
+      wave_fence();
+      if (lane < p.groups)
+        for (int i = 0; i < p.per_group; ++i) merge_top2(a, b, keys[wave][lane * p.per_group + i], 0u);
     }
-    __builtin_amdgcn_wave_barrier();
-    int before = 0;
-    if (lane < p.groups)
-      for (int g = 0; g < p.groups; ++g) {
-        const uint32_t other = gkeys[wave][g];
-        before += other > mine || (other == mine && g < lane);
-      }
-    const uint64_t kept = __ballot(lane < p.groups && before < p.topk_groups && mine != 0u);
+    const uint32_t score = a == 0u ? 0u : p.group_top == 2 && b != 0u ? order_of(of_order(a) + of_order(b)) : a;
+    int before = 0;  // groups that come first
+    for (int g = 0; g < p.groups; ++g) {
+      const uint32_t other = lane_value(score, whole ? g << p.group_shift : g);
+      before += other > score || (other == score && g < mine);
+    }
+    const bool stays = before < p.topk_groups && mine < p.groups && score != 0u;
+    const uint64_t kept = __ballot(stays);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      if (e < p.experts && !((kept >> (e / per)) & 1)) key[i] = 0u;
+      bool in = stays;
+      if (!whole) {
+        const int g = (lane * V + i) / p.per_group;
+        in = g < 64 && ((kept >> g) & 1);
+      }
+      // Without a bias the groups go by scores, the experts by their logits.
+      const uint32_t k = BIAS ? key[i] : order_of(x[i]);
+      key[i] = in ? k : 0u;
     }
   }
 
-  // topk rounds of a maximum over (key, lowest expert).
-  int my_id = -1;
-  float my_score = 0.0f, total = 0.0f;
+  // Largest first within the lane, equal keys in order: as many passes as
+  // experts are wanted.
+#pragma unroll
+  for (int pass = 0; pass < V - 1; ++pass) {
+    if (pass < p.topk) {
+#pragma unroll
+      for (int i = V - 2; i >= pass; --i) {
+        const uint32_t a = key[i], b = key[i + 1];
+        const int ia = idx[i], ib = idx[i + 1];
+        const bool swap = b > a;
+        key[i] = umax(a, b), key[i + 1] = umin(a, b);
+        idx[i] = swap ? ib : ia, idx[i + 1] = swap ? ia : ib;
+      }
+    }
+  }
+  // Each round takes the largest head of all lanes, the lowest lane among
+  // equals, and moves that lane's list up; the order of its registers is kept as
+  // four bits each.
+  uint64_t order = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) order |= (uint64_t)idx[i] << (4 * i);
+  int id = -1;
   for (int j = 0; j < p.topk; ++j) {
-    uint64_t best = 0;
+    const uint32_t best = wave_max(key[0]);
+    if (best == 0u) break;
+    const int from = __builtin_ctzll(__ballot(key[0] == best));
+    const int e = from * V + (__builtin_amdgcn_readlane((int)order, from) & 15);
+    id = lane == j ? e : id;
+    const bool pop = lane == from;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const uint64_t c = key[i] ? ((uint64_t)key[i] << 32) | (uint32_t)~(lane + 64 * i) : 0ull;
-      best = c > best ? c : best;
+      const uint32_t same = key[i], next = i + 1 < V ? key[i + 1] : 0u;
+      key[i] = pop ? next : same;
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint64_t other = __shfl_xor((unsigned long long)best, off, 64);
-      best = other > best ? other : best;
-    }
-    if (best == 0) break;  // the same in every lane
-    const int e = (int)~(uint32_t)best;
-    float sc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e == lane + 64 * i) {
-        sc = s[i];
-        key[i] = 0u;
-      }
-    sc = __shfl(sc, e & 63, 64);
-    total += sc;
-    if (lane == j) {
-      my_id = e;
-      my_score = sc;
-    }
+    if (V > 8) order = pop ? order >> 4 : order;
+    else order = pop ? (uint32_t)order >> 4 : (uint32_t)order;
+  }
+  wave_fence();
+  float w = id >= 0 ? lds[wave][id] : 0.0f;
+  if (p.renormalize) {
+    const float total = wave_sum(w);
+    w = total > 0.0f || total != total ? w / total : 0.0f;
   }
   if (lane < p.topk) {
-    float w = p.scale * my_score;
-    if (p.renormalize) w = total > 0.0f || total != total ? w / total : 0.0f;
-    p.ids[t * p.topk + lane] = my_id;
-    p.weights[t * p.topk + lane] = w;
+    p.ids[t * p.topk + lane] = id;
+    p.weights[t * p.topk + lane] = p.scale * w;
   }
 }
 
-template <typename T, int V>
+// The sigmoid's gradient touches the chosen experts alone and reads only their
+// logits; the softmax's needs the row.  The row of the outputs is put together
+// in shared memory.
+template <bool VEC, typename T, int V, bool SIGMOID>
 __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float lds[kWaves][64 * V];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float x[V], s[V];
+  float* mine = lds[wave] + lane * V;
+  int id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
+  if (id >= p.experts) id = -1;
+  float g = id >= 0 ? p.scale * p.dweights[t * p.topk + lane] : 0.0f;
+  float x[V], s[V], sel = 0.0f;
+  if constexpr (SIGMOID) {
+    if (id >= 0) sel = sigmoid(widen(row[id])).sig;
+  } else {
+    load_row<VEC>(row, p.experts, lane, x);
+    scores<V>(x, s, false);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < p.experts ? load_logit(row + e) : -INFINITY;
+    for (int i = 0; i < V; ++i) mine[i] = s[i];
+    wave_fence();
+    if (id >= 0) sel = lds[wave][id];
   }
-  scores<V>(x, s, p.experts, lane, p.sigmoid != 0);
-
-  int id = -1;
-  float dw = 0.0f;
-  if (lane < p.topk) {
-    id = p.ids[t * p.topk + lane];
-    if (id < 0 || id >= p.experts) id = -1;
-    dw = id >= 0 ? p.dweights[t * p.topk + lane] : 0.0f;
-  }
-  // Lane j takes the score of its expert.
-  float sel = 0.0f;
-  for (int j = 0; j < p.topk; ++j) {
-    const int e = __shfl(id, j, 64);
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i == (e >> 6)) v = s[i];
-    v = __shfl(v, e & 63, 64);
-    if (lane == j && e >= 0) sel = v;
-  }
-  float g = p.scale * dw;
   if (p.renormalize) {
     const float total = wave_sum(sel);
     if (total != 0.0f) g = (g - wave_sum(g * sel) / total) / total;
+    if (id < 0) g = 0.0f;
   }
-  if (id < 0) g = 0.0f;
-  float full[V];
+  wave_fence();
 #pragma unroll
-  for (int i = 0; i < V; ++i) full[i] = 0.0f;
-  for (int j = 0; j < p.topk; ++j) {
-    const int e = __shfl(id, j, 64);
-    const float v = __shfl(g, j, 64);
+  for (int i = 0; i < V; ++i) mine[i] = 0.0f;
+  wave_fence();
+  if (id >= 0) lds[wave][id] = SIGMOID ? g * sel * (1.0f - sel) : g;
+  wave_fence();
+  const float mean = SIGMOID ? 0.0f : wave_sum(g * sel);
+  Pack<T, V> out;
+#pragma unroll
+  for (int i = 0; i < V; ++i) narrow(out.v[i], SIGMOID ? mine[i] : s[i] * (mine[i] - mean));
+  T* to = static_cast<T*>(p.dlogits) + t * p.ld_d + lane * V;
+  if constexpr (VEC) {
+    if (lane * V < p.experts) *reinterpret_cast<Pack<T, V>*>(to) = out;
+  } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e == lane + 64 * i) full[i] = v;
+      if (lane * V + i < p.experts) to[i] = out.v[i];
   }
-  const float mean = p.sigmoid ? 0.0f : wave_sum(g * sel);
-  T* out = static_cast<T*>(p.dlogits) + t * p.ld_d;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    const float dx = p.sigmoid ? full[i] * s[i] * (1.0f - s[i]) : s[i] * (full[i] - mean);
-    if (e < p.experts) store_logit(out + e, dx);
+}
+
+template <bool VEC, typename T, int V>
+void go(const RouteParams& p, bool bwd, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)p.tokens + kWaves - 1) / kWaves)), block(64 * kWaves);
+  if (!bwd) {
+    if (p.bias && p.groups > 1) hipLaunchKernelGGL((route_kernel<VEC, T, V, true, true>), grid, block, 0, stream, p);
+    else if (p.bias) hipLaunchKernelGGL((route_kernel<VEC, T, V, true, false>), grid, block, 0, stream, p);
+    else if (p.groups > 1) hipLaunchKernelGGL((route_kernel<VEC, T, V, false, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((route_kernel<VEC, T, V, false, false>), grid, block, 0, stream, p);
+  } else if (p.sigmoid) hipLaunchKernelGGL((route_bwd_kernel<VEC, T, V, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((route_bwd_kernel<VEC, T, V, false>), grid, block, 0, stream, p);
+}
+
+// Whole vectors: no ragged last lane, and every row starts on a vector.
+template <typename T, int V>
+void go(RouteParams p, bool bwd, hipStream_t stream) {
+  p.group_shift = -1;
+  if (!bwd) {
+    p.per_group = p.experts / p.groups;
+    for (int shift = 0; shift < 6; ++shift)
+      if (p.per_group == V << shift) p.group_shift = shift;
   }
+  constexpr size_t kAlign = alignof(Pack<T, V>);
+  auto fits = [&](const void* at, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(at) % kAlign == 0 && ld * sizeof(T) % kAlign == 0;
+  };
+  const bool vec = p.experts % V == 0 && fits(p.logits, p.ld) && (!bwd || fits(p.dlogits, p.ld_d)) &&
+                   reinterpret_cast<uintptr_t>(p.bias) % alignof(Pack<float, V>) == 0;
+  if (vec) go<true, T, V>(p, bwd, stream);
+  else go<false, T, V>(p, bwd, stream);
 }
 
 template <typename T>
 hipError_t pick(const RouteParams& p, bool bwd, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)p.tokens + kWaves - 1) / kWaves)), block(64 * kWaves);
-  auto go = [&](auto fwd, auto grad) {
-    if (bwd) hipLaunchKernelGGL(grad, grid, block, 0, stream, p);
-    else hipLaunchKernelGGL(fwd, grid, block, 0, stream, p);
-  };
   const int v = (p.experts + 63) / 64;
-  if (v <= 1) go(route_kernel<T, 1>, route_bwd_kernel<T, 1>);
-  else if (v <= 2) go(route_kernel<T, 2>, route_bwd_kernel<T, 2>);
-  else if (v <= 4) go(route_kernel<T, 4>, route_bwd_kernel<T, 4>);
-  else if (v <= 8) go(route_kernel<T, 8>, route_bwd_kernel<T, 8>);
-  else go(route_kernel<T, 16>, route_bwd_kernel<T, 16>);
+  if (v <= 1) go<T, 1>(p, bwd, stream);
+  else if (v <= 2) go<T, 2>(p, bwd, stream);
+  else if (v <= 4) go<T, 4>(p, bwd, stream);
+  else if (v <= 8) go<T, 8>(p, bwd, stream);
+  else go<T, 16>(p, bwd, stream);
   return hipGetLastError();
 }
 

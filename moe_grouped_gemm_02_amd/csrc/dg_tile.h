@@ -2,16 +2,9 @@
 // quantised along its rows and, transposed, along its columns.
 #pragma once
 
-#include "dg_device.h"
+#include "dg_math.h"
 
 namespace dg {
-
-// 1 / d for normal d, within about half an ulp: the hardware's (1 ulp) and one
-// Newton step.
-__device__ __forceinline__ float reciprocal(float d) {
-  const float y = __builtin_amdgcn_rcpf(d);
-  return fmaf(fmaf(-d, y, 1.0f), y, y);
-}
 
 // Scale and its inverse for float32 values: s = amax / 448 (a product with one
 // correction by its residual), kept normal (at least 2^-126) so that its
@@ -33,27 +26,6 @@ __device__ __forceinline__ TileScale tile_scale(float amax) {
 __device__ __forceinline__ uint32_t ue8m0_exponent_f32(float amax) {
   const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
   return (uint32_t)(e < 0 ? 0 : e);
-}
-
-// exp(v) for v up to 80 (larger ones as 80): 2^k 2^f with k the integer next
-// to v log2(e), so that f carries none of the rounding of that product and
-// results below the normal range come out rounded, not as zero.
-__device__ __forceinline__ float exp_to_80(float v) {
-  v = fminf(v, 80.0f);
-  const float k = __builtin_rintf(v * 1.44269504088896340736f);
-  const float f = fmaf(v, 1.44269504088896340736f, -k);
-  return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)k);
-}
-
-// sigmoid(v) = e^v / (1 + e^v): the e^v in front keeps its relative accuracy
-// for large negative v.
-struct Sigmoid {
-  float e, n, sig;  // e^v, 1 / (1 + e^v), their product
-};
-__device__ __forceinline__ Sigmoid sigmoid(float v) {
-  const float e = exp_to_80(v);
-  const float n = reciprocal(1.0f + e);
-  return {e, n, e * n};
 }
 
 // d silu / dv = sig (1 + v (1 - sig)) = sig n (1 + v + e^v) at v = code * scale.
