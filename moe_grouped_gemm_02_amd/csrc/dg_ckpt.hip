@@ -112,20 +112,30 @@ __device__ __forceinline__ void decode8(const uint8_t* q, float (&v)[8]) {
   }
 }
 
+// Rows in use among the thread's R rows from row r on, as bits.
+template <int R>
+__device__ __forceinline__ uint32_t rows_in_use(const int32_t* m_indices, int64_t r) {
+  uint32_t live = (1u << R) - 1u;
+  if (m_indices) {
+    live = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) live |= (m_indices[r + i] >= 0 ? 1u : 0u) << i;
+  }
+  return live;
+}
+
 // Workgroup (x, y): rows [128 x, 128 x + 128), gate and up tile y.
-__global__ __launch_bounds__(kTileThreads) void swiglu_bwd_kernel(SwigluBwdParams p) {
-  __shared__ TileLds lds;
+template <int R>
+__global__ __launch_bounds__(kTileThreads<R>) void swiglu_bwd_kernel(SwigluBwdParams p) {
+  __shared__ TileLds<R> lds;
   const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
   const int tiles = p.inter / kBlockK, j = blockIdx.y, col0 = j * kBlockK;
-  const int tid = threadIdx.x, r0 = (tid >> 4) * 4, c0 = (tid & 15) * 8;
-  uint32_t live = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (!p.m_indices || p.m_indices[row0 + r0 + i] >= 0) live |= 1u << i;
+  const int tid = threadIdx.x, r0 = (tid >> 4) * R, c0 = (tid & 15) * 8;
+  const uint32_t live = rows_in_use<R>(p.m_indices, row0 + r0);
   if (!__syncthreads_or(live != 0)) return;
-  float dg[4][8], du[4][8], act[4][8];
+  float dg[R][8], du[R][8], act[R][8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     float gate[8], up[8], da[8], gate_s = 0.0f, up_s = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) gate[c] = up[c] = da[c] = 0.0f;
@@ -151,40 +161,39 @@ __global__ __launch_bounds__(kTileThreads) void swiglu_bwd_kernel(SwigluBwdParam
       dg[i][c] = da[c] * u * silu_slope(gate[c], gate_s, g, sg);
     }
   }
-  tile_rows(dg, p.dq + row0 * 2 * p.inter + col0, 2 * (int64_t)p.inter, p.dsf + j * p.ld_dsf + row0, live);
-  tile_rows(du, p.dq + row0 * 2 * p.inter + p.inter + col0, 2 * (int64_t)p.inter,
-            p.dsf + (tiles + j) * p.ld_dsf + row0, live);
+  const int64_t ld = 2 * (int64_t)p.inter;
+  tile_rows<R>(dg, p.dq + row0 * ld + col0, ld, p.dsf + j * p.ld_dsf + row0, live);
+  tile_rows<R>(du, p.dq + row0 * ld + p.inter + col0, ld, p.dsf + (tiles + j) * p.ld_dsf + row0, live);
   float* dsft = p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0;
-  tile_columns(dg, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, dsft);
-  tile_columns(du, lds, p.dqt + (int64_t)(p.inter + col0) * p.m_total + row0, p.m_total, dsft + p.inter);
+  tile_columns<R>(dg, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, dsft);
+  tile_columns<R>(du, lds, p.dqt + (int64_t)(p.inter + col0) * p.m_total + row0, p.m_total, dsft + p.inter);
   if (p.aqt)
-    tile_columns(act, lds, p.aqt + (int64_t)col0 * p.m_total + row0, p.m_total,
-                 p.asft + (int64_t)blockIdx.x * p.ld_asft + col0);
+    tile_columns<R>(act, lds, p.aqt + (int64_t)col0 * p.m_total + row0, p.m_total,
+                    p.asft + (int64_t)blockIdx.x * p.ld_asft + col0);
 }
 
 // Workgroup (x, y): rows [128 x, 128 x + 128), column tile y.
-__global__ __launch_bounds__(kTileThreads) void requant_t_kernel(RequantParams p) {
-  __shared__ TileLds lds;
+__global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParams p) {
+  __shared__ TileLds<8> lds;
   const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
   const int col0 = blockIdx.y * kBlockK;
-  const int tid = threadIdx.x, r0 = (tid >> 4) * 4, c0 = (tid & 15) * 8;
-  float v[4][8];
-  bool any = false;
+  const int tid = threadIdx.x, r0 = (tid >> 4) * 8, c0 = (tid & 15) * 8;
+  const uint32_t live = rows_in_use<8>(p.m_indices, row0 + r0);
+  float v[8][8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const int64_t r = row0 + r0 + i;
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[i][c] = 0.0f;
-    if (!p.m_indices || p.m_indices[r] >= 0) {
-      any = true;
+    if ((live >> i) & 1) {
       decode8(p.q + r * p.cols + col0 + c0, v[i]);
       const float s = p.sf[blockIdx.y * p.ld_sf + r];
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[i][c] *= s;
     }
   }
-  if (!__syncthreads_or(any)) return;
-  tile_columns(v, lds, p.qt + (int64_t)col0 * p.rows + row0, p.rows, p.sft + (int64_t)blockIdx.x * p.ld_sft + col0);
+  if (!__syncthreads_or(live != 0)) return;
+  tile_columns<8>(v, lds, p.qt + (int64_t)col0 * p.rows + row0, p.rows, p.sft + (int64_t)blockIdx.x * p.ld_sft + col0);
 }
 
 }  // namespace
@@ -203,12 +212,12 @@ hipError_t launch_swiglu_quant(const SwigluParams& p, bool pow2, hipStream_t str
 }
 
 hipError_t launch_swiglu_bwd(const SwigluBwdParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(p.m_total / kBlockK, p.inter / kBlockK), dim3(kTileThreads), 0, stream, p);
+  hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3(p.m_total / kBlockK, p.inter / kBlockK), dim3(kTileThreads<4>), 0, stream, p);
   return hipGetLastError();
 }
 
 hipError_t launch_requant_t(const RequantParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(requant_t_kernel, dim3(p.rows / kBlockK, p.cols / kBlockK), dim3(kTileThreads), 0, stream, p);
+  hipLaunchKernelGGL(requant_t_kernel, dim3(p.rows / kBlockK, p.cols / kBlockK), dim3(kTileThreads<8>), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -205,46 +205,51 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
 }
 
 // Workgroup (x, y): rows [128 x, 128 x + 128), columns [128 y, 128 y + 128).
-__global__ __launch_bounds__(kTileThreads) void combine_bwd_kernel(CombineBwdParams p) {
-  __shared__ TileLds lds;
+__global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwdParams p) {
+  __shared__ TileLds<8> lds;
   const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
   const int col0 = blockIdx.y * kBlockK;
-  const int tid = threadIdx.x, r0 = (tid >> 4) * 4, c0 = (tid & 15) * 8;
+  const int tid = threadIdx.x, r0 = (tid >> 4) * 8, i16 = tid & 15, c0 = i16 * 8;
   const int64_t entries = (int64_t)p.tokens * p.topk;
-  float v[4][8];
+  float v[8][8];
   uint32_t live = 0;
+  uint4 a[8], b[8];
+  float w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const int64_t r = row0 + r0 + i;
     const int e = p.src[r];
-    const bool used = e >= 0 && e < entries;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    float w = 0.0f;
-    if (used) {
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    w[i] = 0.0f;
+    if (e >= 0 && e < entries) {
       live |= 1u << i;
-      a = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / p.topk) * p.ld_dy + col0 + c0);
-      b = *reinterpret_cast<const uint4*>(p.d + r * p.ld_d + col0 + c0);
-      w = p.weights[e];
+      a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / p.topk) * p.ld_dy + col0 + c0);
+      b[i] = *reinterpret_cast<const uint4*>(p.d + r * p.ld_d + col0 + c0);
+      w[i] = p.weights[e];
     }
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  }
+  float mine = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float x0 = bf16_bits_to_f32(x[c] & 0xFFFFu), x1 = bf16_bits_to_f32(x[c] >> 16);
       dot = fmaf(x0, bf16_bits_to_f32(y[c] & 0xFFFFu), dot);
       dot = fmaf(x1, bf16_bits_to_f32(y[c] >> 16), dot);
-      v[i][2 * c] = w * x0;
-      v[i][2 * c + 1] = w * x1;
+      v[i][2 * c] = w[i] * x0;
+      v[i][2 * c + 1] = w[i] * x1;
     }
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) dot += __shfl_xor(dot, off, 16);
-    if (used && c0 == 0) p.dots[r * (p.cols / kBlockK) + blockIdx.y] = dot;
+    dot = row_sum(dot);
+    mine = i16 == i ? dot : mine;
   }
-  tile_rows(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + blockIdx.y * p.ld_dsf + row0, live);
+  if (i16 < 8 && ((live >> i16) & 1)) p.dots[(row0 + r0 + i16) * (p.cols / kBlockK) + blockIdx.y] = mine;
+  tile_rows<8>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + blockIdx.y * p.ld_dsf + row0, live);
   if (!p.dqt) return;
   if (!__syncthreads_or(live != 0)) return;
-  tile_columns(v, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total,
-               p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0);
+  tile_columns<8>(v, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total,
+                  p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0);
 }
 
 // dweights of each entry: 16 lanes add the dot products of its row's tiles.
@@ -308,7 +313,7 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
 
 hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream) {
   if (p.m_total > 0)
-    hipLaunchKernelGGL(combine_bwd_kernel, dim3(p.m_total / kBlockK, p.cols / kBlockK), dim3(kTileThreads), 0, stream, p);
+    hipLaunchKernelGGL(combine_bwd_kernel, dim3(p.m_total / kBlockK, p.cols / kBlockK), dim3(kTileThreads<8>), 0, stream, p);
   const int64_t entries = (int64_t)p.tokens * p.topk;
   hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)((entries + 15) / 16)), dim3(256), 0, stream, p);
   return hipGetLastError();

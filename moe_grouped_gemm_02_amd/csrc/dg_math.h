@@ -2,6 +2,8 @@
 // stay in the registers of a wave.
 #pragma once
 
+#include <utility>
+
 #include "dg_device.h"
 
 namespace dg {
@@ -44,6 +46,16 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// f(0) .. f(N - 1) with the index as a type, for what must be a constant.
+template <int... I, typename F>
+__device__ __forceinline__ void for_each_index(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_each_index(F&& f) {
+  for_each_index(std::make_integer_sequence<int, N>{}, f);
+}
+
 // v of the lane that CTRL names, inside a row of 16 lanes or from one row to the
 // next; 0 where that lane does not exist.
 template <int CTRL>
@@ -56,6 +68,7 @@ __device__ __forceinline__ float dpp(float v) {
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;                  // quad_perm
 constexpr int kHalfMirror = 0x141, kRowMirror = 0x140;     // the other quad of 8 lanes, the other half of 16
+constexpr int kRowLane0 = 0x150;                           // + n: lane n of the row, to all of it
 constexpr int kBroadcast15 = 0x142, kBroadcast31 = 0x143;  // a row's last lane to the next row, lane 31 to rows 2, 3
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -90,11 +103,15 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = umax(v, dpp<kBroadcast31>(v));
   return lane_value(v, 63);
 }
-__device__ __forceinline__ float wave_sum(float v) {
+// Over the 16 lanes of a row, in each of them.
+__device__ __forceinline__ float row_sum(float v) {
   v += dpp<kXor1>(v);
   v += dpp<kXor2>(v);
   v += dpp<kHalfMirror>(v);
-  v += dpp<kRowMirror>(v);
+  return v + dpp<kRowMirror>(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum(v);
   return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 

@@ -44,74 +44,127 @@ __device__ __forceinline__ float silu_slope(float code, float scale, float v, co
   return s.sig * s.n * (fabsf(u) < 0.0625f ? near : far);
 }
 
-// Tile kernels: 512 threads, thread t holds rows 4 (t / 16) .. + 3 and columns
-// 8 (t % 16) .. + 7 of a 128 x 128 tile, so a row of the tile is 16 lanes and
-// four rows of a column are the four bytes of a word of the transposed codes.
-constexpr int kTileThreads = 512;
+// 128 x 128 tiles.  Thread t of the workgroup holds R rows, R (t / 16) on, and
+// 8 columns, 8 (t % 16) on: a row of the tile is 16 lanes, a row of the
+// hardware's row operations, and the R rows of a column are R bytes of the
+// transposed codes.  R = 8 takes 256 threads, R = 4 512.
+template <int R>
+constexpr int kTileThreads = kBlockK * kBlockK / (8 * R);
 
+template <int R>
 struct TileLds {
-  float colmax[8][kBlockK];                 // a wave's maximum of each column
-  uint32_t codes[kBlockK][kBlockK / 4 + 1];  // transposed codes, four rows a word
+  static constexpr int kGroups = kBlockK / R;
+  // Maximum of each column over each group of R rows; the padding keeps the two
+  // (four) parts of a column that are read together on different banks.
+  float partial[kGroups][kBlockK + 4];
+  float inv[kBlockK];
+  alignas(16) uint8_t codes[kBlockK * kBlockK];
 };
 
-// Row-wise codes of the thread's 4 x 8 values: q points at the tile's first row
-// and column (row stride ldq), sf at the scale of its first row.  Rows with
-// their bit clear in `live` are not written.
-__device__ __forceinline__ void tile_rows(const float (&v)[4][8], uint8_t* q, int64_t ldq, float* sf, uint32_t live) {
-  const int r0 = (threadIdx.x >> 4) * 4, c0 = (threadIdx.x & 15) * 8;
+// Where byte 16 `chunk` of column `col` lies in TileLds::codes.  Lanes write
+// columns 8 apart and read 8 columns of 8 chunks: the exclusive-ors spread the
+// first over all banks and leave the second a permutation of 1 KB.
+__device__ __forceinline__ int codes_at(int col, int chunk) {
+  return (col ^ ((col >> 6) & 1)) * kBlockK + (chunk ^ ((col >> 3) & 7)) * 16;
+}
+
+// Scale and inverse of each of the thread's rows: lane i of the 16 (i < R)
+// computes row i's, so that the rows' divisions are made once, not by all lanes;
+// row i's inverse is then v of lane i.
+template <int R>
+__device__ __forceinline__ TileScale row_scale_of_lane(const float (&v)[R][8]) {
+  const int i16 = threadIdx.x & 15;
+  uint32_t mine = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float amax = 0.0f;
+  for (int i = 0; i < R; ++i) {
+    float m = fmaxf(fabsf(v[i][0]), fabsf(v[i][1]));
 #pragma unroll
-    for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[i][c]));
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 16));
-    const TileScale t = tile_scale(amax);
-    if ((live >> i) & 1) {
-      const uint32_t lo = e4m3_x4(v[i][0] * t.inv, v[i][1] * t.inv, v[i][2] * t.inv, v[i][3] * t.inv);
-      const uint32_t hi = e4m3_x4(v[i][4] * t.inv, v[i][5] * t.inv, v[i][6] * t.inv, v[i][7] * t.inv);
-      *reinterpret_cast<uint2*>(q + (int64_t)(r0 + i) * ldq + c0) = make_uint2(lo, hi);
-      if (c0 == 0) sf[r0 + i] = t.s;
-    }
+    for (int c = 2; c < 8; c += 2) m = fmaxf(m, fmaxf(fabsf(v[i][c]), fabsf(v[i][c + 1])));
+    uint32_t u = __float_as_uint(m);  // not negative: ordered like its bits
+    u = umax(u, dpp<kXor1>(u));
+    u = umax(u, dpp<kXor2>(u));
+    u = umax(u, dpp<kHalfMirror>(u));
+    u = umax(u, dpp<kRowMirror>(u));
+    mine = i16 == i ? u : mine;
   }
+  return tile_scale(__uint_as_float(mine));
+}
+
+// Row-wise codes of the thread's values: q points at the tile's first row and
+// column (row stride ldq), sf at the scale of its first row.  Rows with their
+// bit clear in `live` are not written.
+template <int R>
+__device__ __forceinline__ void tile_rows(const float (&v)[R][8], uint8_t* q, int64_t ldq, float* sf, uint32_t live) {
+  const int r0 = (threadIdx.x >> 4) * R, c0 = (threadIdx.x & 15) * 8, i16 = threadIdx.x & 15;
+  const TileScale t = row_scale_of_lane<R>(v);
+  if (i16 < R && ((live >> i16) & 1)) sf[r0 + i16] = t.s;
+  q += (int64_t)r0 * ldq + c0;
+  auto row = [&](auto index) {
+    constexpr int i = decltype(index)::value;
+    const float inv = dpp<kRowLane0 + i>(t.inv);
+    const uint32_t lo = e4m3_x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+    const uint32_t hi = e4m3_x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+    if ((live >> i) & 1) *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
+    q += ldq;
+  };
+  for_each_index<R>(row);
 }
 
 // Transposed codes of the tile, one scale per column: q points at the tile's
 // first column (as a row of the transposed matrix, row stride ldq) and first
 // row, sf at the scale of its first column.  Every thread of the workgroup
 // calls it; values of rows not in use must be zero.
-__device__ __forceinline__ void tile_columns(const float (&v)[4][8], TileLds& lds, uint8_t* q, int64_t ldq, float* sf) {
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int c0 = (tid & 15) * 8;
+template <int R>
+__device__ __forceinline__ void tile_columns(const float (&v)[R][8], TileLds<R>& lds, uint8_t* q, int64_t ldq, float* sf) {
+  constexpr int kParts = kTileThreads<R> / kBlockK;  // threads that share a column's maximum
+  const int tid = threadIdx.x, group = tid >> 4, c0 = (tid & 15) * 8;
   float amax[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    amax[c] = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
-    amax[c] = fmaxf(amax[c], __shfl_xor(amax[c], 16, 64));
-    amax[c] = fmaxf(amax[c], __shfl_xor(amax[c], 32, 64));
-  }
-  __syncthreads();  // the last use of lds is over
-  if ((tid & 63) < 16) {
+    amax[c] = fmaxf(fabsf(v[0][c]), fabsf(v[1][c]));
 #pragma unroll
-    for (int c = 0; c < 8; ++c) lds.colmax[wave][c0 + c] = amax[c];
+    for (int i = 2; i < R; i += 2) amax[c] = fmaxf(amax[c], fmaxf(fabsf(v[i][c]), fabsf(v[i + 1][c])));
   }
+  float4* to = reinterpret_cast<float4*>(&lds.partial[group][c0]);
+  to[0] = make_float4(amax[0], amax[1], amax[2], amax[3]);
+  to[1] = make_float4(amax[4], amax[5], amax[6], amax[7]);
   __syncthreads();
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  {
+    const int col = tid / kParts, part = tid % kParts;
     float m = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, lds.colmax[w][c0 + c]);
-    const TileScale t = tile_scale(m);
-    lds.codes[c0 + c][tid >> 4] = e4m3_x4(v[0][c] * t.inv, v[1][c] * t.inv, v[2][c] * t.inv, v[3][c] * t.inv);
-    if (tid < 16) sf[c0 + c] = t.s;
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, lds.partial[part * 8 + i][col]);
+    uint32_t u = __float_as_uint(m);
+    u = umax(u, dpp<kXor1>(u));
+    if (kParts == 4) u = umax(u, dpp<kXor2>(u));
+    const TileScale t = tile_scale(__uint_as_float(u));
+    if (part == 0) {
+      lds.inv[col] = t.inv;
+      sf[col] = t.s;
+    }
+  }
+  __syncthreads();
+  const float4 i0 = *reinterpret_cast<const float4*>(&lds.inv[c0]), i1 = *reinterpret_cast<const float4*>(&lds.inv[c0 + 4]);
+  const float inv[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint8_t* at = lds.codes + codes_at(c0 + c, group * R / 16) + group * R % 16;
+    const uint32_t lo = e4m3_x4(v[0][c] * inv[c], v[1][c] * inv[c], v[2][c] * inv[c], v[3][c] * inv[c]);
+    if constexpr (R == 8) {
+      const uint32_t hi = e4m3_x4(v[4][c] * inv[c], v[5][c] * inv[c], v[6][c] * inv[c], v[7][c] * inv[c]);
+      *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi);
+    } else {
+      *reinterpret_cast<uint32_t*>(at) = lo;
+    }
   }
   __syncthreads();
   // 8 lanes write the 128 codes of a column.
+  constexpr int kColumns = kTileThreads<R> / 8;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int col = i * 64 + (tid >> 3), w = (tid & 7) * 4;
-    const uint32_t* p = &lds.codes[col][w];
-    *reinterpret_cast<uint4*>(q + (int64_t)col * ldq + w * 4) = make_uint4(p[0], p[1], p[2], p[3]);
+  for (int i = 0; i < kBlockK / kColumns; ++i) {
+    const int col = i * kColumns + (tid >> 3), chunk = tid & 7;
+    *reinterpret_cast<uint4*>(q + (int64_t)col * ldq + chunk * 16) =
+        *reinterpret_cast<const uint4*>(lds.codes + codes_at(col, chunk));
   }
 }
 
