@@ -97,10 +97,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) 
   }
 }
 
-// The thread's 8 codes of a row as numbers.
-__device__ __forceinline__ void decode8(const uint8_t* q, float (&v)[8]) {
+// 8 codes as numbers.
+__device__ __forceinline__ void decode8(uint2 w, float (&v)[8]) {
   typedef float v2f __attribute__((ext_vector_type(2)));
-  const uint2 w = *reinterpret_cast<const uint2*>(q);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int word = (int)(h ? w.y : w.x);
@@ -112,88 +111,126 @@ __device__ __forceinline__ void decode8(const uint8_t* q, float (&v)[8]) {
   }
 }
 
-// Rows in use among the thread's R rows from row r on, as bits.
-template <int R>
-__device__ __forceinline__ uint32_t rows_in_use(const int32_t* m_indices, int64_t r) {
-  uint32_t live = (1u << R) - 1u;
-  if (m_indices) {
-    live = 0;
+// What a thread reads of one tile: its 4 rows x 8 columns of gate and up codes
+// and of dact, and the rows' scales.
+struct SwigluBwdRaw {
+  uint2 gate[4], up[4];
+  uint4 da[4];
+  float gate_s[4], up_s[4];
+};
+
+__device__ __forceinline__ void load_raw(const SwigluBwdParams& p, TileAt tile, SwigluBwdRaw& raw) {
+  const int tiles = p.inter / kBlockK;
+  const int64_t row = (int64_t)tile.row * kBlockK + (threadIdx.x >> 4) * 4;
+  const int col = tile.col * kBlockK + (threadIdx.x & 15) * 8;
+  const uint8_t* hq = p.hq + row * 2 * p.inter + col;
+  const uint16_t* dact = p.dact + row * p.ld_dact + col;
 #pragma unroll
-    for (int i = 0; i < R; ++i) live |= (m_indices[r + i] >= 0 ? 1u : 0u) << i;
+  for (int i = 0; i < 4; ++i) {
+    raw.gate[i] = *reinterpret_cast<const uint2*>(hq + (int64_t)i * 2 * p.inter);
+    raw.up[i] = *reinterpret_cast<const uint2*>(hq + (int64_t)i * 2 * p.inter + p.inter);
+    raw.da[i] = *reinterpret_cast<const uint4*>(dact + i * p.ld_dact);
   }
-  return live;
+  load_floats<4>(p.hsf + tile.col * p.ld_hsf + row, raw.gate_s);
+  load_floats<4>(p.hsf + (tiles + tile.col) * p.ld_hsf + row, raw.up_s);
 }
 
-// Workgroup (x, y): rows [128 x, 128 x + 128), gate and up tile y.
-template <int R>
-__global__ __launch_bounds__(kTileThreads<R>) void swiglu_bwd_kernel(SwigluBwdParams p) {
-  __shared__ TileLds<R> lds;
-  const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
-  const int tiles = p.inter / kBlockK, j = blockIdx.y, col0 = j * kBlockK;
-  const int tid = threadIdx.x, r0 = (tid >> 4) * R, c0 = (tid & 15) * 8;
-  const uint32_t live = rows_in_use<R>(p.m_indices, row0 + r0);
-  if (!__syncthreads_or(live != 0)) return;
-  float dg[R][8], du[R][8], act[R][8];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float gate[8], up[8], da[8], gate_s = 0.0f, up_s = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) gate[c] = up[c] = da[c] = 0.0f;
-    if ((live >> i) & 1) {
-      const int64_t r = row0 + r0 + i;
-      const uint8_t* hq = p.hq + r * 2 * p.inter + col0 + c0;
-      decode8(hq, gate);
-      decode8(hq + p.inter, up);
-      gate_s = p.hsf[j * p.ld_hsf + r];
-      up_s = p.hsf[(tiles + j) * p.ld_hsf + r];
-      const uint4 d = *reinterpret_cast<const uint4*>(p.dact + r * p.ld_dact + col0 + c0);
-      const uint32_t b[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) da[c] = bf16_bits_to_f32((c & 1) ? b[c >> 1] >> 16 : b[c >> 1] & 0xFFFFu);
+// Workgroups walk over tiles of 128 rows x 128 gate columns and the same up
+// columns, 32 workgroups of an XCD over its eighth of the tiles (row tiles
+// fastest).  The three results of a tile stay in registers (96 of a thread)
+// while their columns' maxima come together, so one workgroup fills a CU; the
+// next tile is read while this one is quantised and written.
+constexpr int kBwdWorkgroups = 256;  // one for each CU
+
+__global__ __launch_bounds__(kTileThreads<4>, 2) void swiglu_bwd_kernel(SwigluBwdParams p) {
+  __shared__ TileLds<4, 3> lds;
+  const int row_tiles = p.m_total / kBlockK, tiles = p.inter / kBlockK;
+  const int all = row_tiles * tiles;
+  // Workgroup b works on XCD b % 8.
+  const int xcds = gridDim.x < 8 ? (int)gridDim.x : 8;
+  const int xcd = blockIdx.x % xcds, mine = blockIdx.x / xcds, peers = ((int)gridDim.x - xcd + xcds - 1) / xcds;
+  const int end = (int)((int64_t)all * (xcd + 1) / xcds);
+  int t = (int)((int64_t)all * xcd / xcds) + mine;
+  // The next tile of this workgroup with rows in use, from t on.
+  auto seek = [&](TileUse& use) {
+    for (; t < end; t += peers) {
+      use = tile_use(p.m_indices ? p.m_indices + (int64_t)(t % row_tiles) * kBlockK : nullptr);
+      if (use.any()) return;
     }
+  };
+  TileUse use;
+  SwigluBwdRaw raw;
+  seek(use);
+  if (t < end) load_raw(p, {t % row_tiles, t / row_tiles}, raw);
+  while (t < end) {
+    const TileAt tile = {t % row_tiles, t / row_tiles};
+    const uint32_t live = use.of_thread<4>();
+    float out[3][4][8];  // d gate, d up, and the unit's output
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float g = gate[c] * gate_s, u = up[c] * up_s;
-      const Sigmoid sg = sigmoid(g);
-      const float silu = g * sg.sig;
-      act[i][c] = silu * u;
-      du[i][c] = da[c] * silu;
-      dg[i][c] = da[c] * u * silu_slope(gate[c], gate_s, g, sg);
+    for (int i = 0; i < 4; ++i) {
+      const bool in = (live >> i) & 1;
+      const uint2 none = make_uint2(0, 0);
+      float gate[8], up[8];
+      decode8(in ? raw.gate[i] : none, gate);
+      decode8(in ? raw.up[i] : none, up);
+      const float gate_s = in ? raw.gate_s[i] : 0.0f, up_s = in ? raw.up_s[i] : 0.0f;
+      const uint4 d = raw.da[i];
+      const uint32_t b[4] = {in ? d.x : 0u, in ? d.y : 0u, in ? d.z : 0u, in ? d.w : 0u};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float da = bf16_bits_to_f32((c & 1) ? b[c >> 1] >> 16 : b[c >> 1] & 0xFFFFu);
+        const float g = gate[c] * gate_s, u = up[c] * up_s;
+        const Sigmoid sg = sigmoid(g);
+        const float silu = g * sg.sig;
+        out[0][i][c] = da * u * silu_slope(gate[c], gate_s, g, sg);
+        out[1][i][c] = da * silu;
+        out[2][i][c] = silu * u;
+      }
     }
+    t += peers;
+    seek(use);
+    if (t < end) load_raw(p, {t % row_tiles, t / row_tiles}, raw);
+    const int64_t row0 = (int64_t)tile.row * kBlockK, ld = 2 * (int64_t)p.inter;
+    const int col0 = tile.col * kBlockK;
+    tile_rows<4>(out[0], p.dq + row0 * ld + col0, ld, p.dsf + tile.col * p.ld_dsf + row0, live);
+    tile_rows<4>(out[1], p.dq + row0 * ld + p.inter + col0, ld, p.dsf + (tiles + tile.col) * p.ld_dsf + row0, live);
+    uint8_t* dqt = p.dqt + (int64_t)col0 * p.m_total + row0;
+    float* dsft = p.dsft + (int64_t)tile.row * p.ld_dsft + col0;
+    const ColumnsTo to[3] = {
+        {dqt, p.m_total, dsft},
+        {dqt + (int64_t)p.inter * p.m_total, p.m_total, dsft + p.inter},
+        {p.aqt ? p.aqt + (int64_t)col0 * p.m_total + row0 : nullptr, p.m_total, p.asft + (int64_t)tile.row * p.ld_asft + col0}};
+    tile_columns(out, lds, to);
   }
-  const int64_t ld = 2 * (int64_t)p.inter;
-  tile_rows<R>(dg, p.dq + row0 * ld + col0, ld, p.dsf + j * p.ld_dsf + row0, live);
-  tile_rows<R>(du, p.dq + row0 * ld + p.inter + col0, ld, p.dsf + (tiles + j) * p.ld_dsf + row0, live);
-  float* dsft = p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0;
-  tile_columns<R>(dg, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, dsft);
-  tile_columns<R>(du, lds, p.dqt + (int64_t)(p.inter + col0) * p.m_total + row0, p.m_total, dsft + p.inter);
-  if (p.aqt)
-    tile_columns<R>(act, lds, p.aqt + (int64_t)col0 * p.m_total + row0, p.m_total,
-                    p.asft + (int64_t)blockIdx.x * p.ld_asft + col0);
 }
 
-// Workgroup (x, y): rows [128 x, 128 x + 128), column tile y.
+// Workgroup: one 128 x 128 tile.
 __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParams p) {
   __shared__ TileLds<8> lds;
-  const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
-  const int col0 = blockIdx.y * kBlockK;
+  const TileAt tile = tile_of_workgroup(p.rows / kBlockK);
+  const int64_t row0 = (int64_t)tile.row * kBlockK;
+  const int col0 = tile.col * kBlockK;
   const int tid = threadIdx.x, r0 = (tid >> 4) * 8, c0 = (tid & 15) * 8;
-  const uint32_t live = rows_in_use<8>(p.m_indices, row0 + r0);
-  float v[8][8];
+  const TileUse use = tile_use(p.m_indices ? p.m_indices + row0 : nullptr);
+  if (!use.any()) return;
+  const uint32_t live = use.of_thread<8>();
+  uint2 q[8];
+  float s[8], vs[1][8][8];
+  auto& v = vs[0];
+  const uint8_t* from = p.q + (row0 + r0) * p.cols + col0 + c0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = *reinterpret_cast<const uint2*>(from + (int64_t)i * p.cols);
+  load_floats<8>(p.sf + tile.col * p.ld_sf + row0 + r0, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + r0 + i;
+    const bool in = (live >> i) & 1;
+    decode8(in ? q[i] : make_uint2(0, 0), v[i]);
+    const float scale = in ? s[i] : 0.0f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[i][c] = 0.0f;
-    if ((live >> i) & 1) {
-      decode8(p.q + r * p.cols + col0 + c0, v[i]);
-      const float s = p.sf[blockIdx.y * p.ld_sf + r];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[i][c] *= s;
-    }
+    for (int c = 0; c < 8; ++c) v[i][c] *= scale;
   }
-  if (!__syncthreads_or(live != 0)) return;
-  tile_columns<8>(v, lds, p.qt + (int64_t)col0 * p.rows + row0, p.rows, p.sft + (int64_t)blockIdx.x * p.ld_sft + col0);
+  const ColumnsTo to[1] = {{p.qt + (int64_t)col0 * p.rows + row0, p.rows, p.sft + (int64_t)tile.row * p.ld_sft + col0}};
+  tile_columns(vs, lds, to);
 }
 
 }  // namespace
@@ -212,12 +249,14 @@ hipError_t launch_swiglu_quant(const SwigluParams& p, bool pow2, hipStream_t str
 }
 
 hipError_t launch_swiglu_bwd(const SwigluBwdParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(swiglu_bwd_kernel<4>, dim3(p.m_total / kBlockK, p.inter / kBlockK), dim3(kTileThreads<4>), 0, stream, p);
+  const int tiles = p.m_total / kBlockK * (p.inter / kBlockK);
+  hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(tiles < kBwdWorkgroups ? tiles : kBwdWorkgroups), dim3(kTileThreads<4>), 0, stream, p);
   return hipGetLastError();
 }
 
 hipError_t launch_requant_t(const RequantParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(requant_t_kernel, dim3(p.rows / kBlockK, p.cols / kBlockK), dim3(kTileThreads<8>), 0, stream, p);
+  const int tiles = p.rows / kBlockK * (p.cols / kBlockK);
+  hipLaunchKernelGGL(requant_t_kernel, dim3(tiles), dim3(kTileThreads<8>), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -204,26 +204,29 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
   *reinterpret_cast<uint4*>(p.y + t * p.ld_y + col) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Workgroup (x, y): rows [128 x, 128 x + 128), columns [128 y, 128 y + 128).
+// Workgroup: one 128 x 128 tile of the expert rows.
 __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwdParams p) {
   __shared__ TileLds<8> lds;
-  const int64_t row0 = (int64_t)blockIdx.x * kBlockK;
-  const int col0 = blockIdx.y * kBlockK;
+  const TileAt tile = tile_of_workgroup(p.m_total / kBlockK);
+  const int64_t row0 = (int64_t)tile.row * kBlockK;
+  const int col0 = tile.col * kBlockK;
   const int tid = threadIdx.x, r0 = (tid >> 4) * 8, i16 = tid & 15, c0 = i16 * 8;
-  const int64_t entries = (int64_t)p.tokens * p.topk;
-  float v[8][8];
+  const TileUse use = tile_use(p.src + row0);
+  if (!use.any()) return;
+  const uint32_t entries = (uint32_t)(p.tokens * p.topk);
+  float vs[1][8][8], w[8];
+  auto& v = vs[0];
   uint32_t live = 0;
   uint4 a[8], b[8];
-  float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = row0 + r0 + i;
-    const int e = p.src[r];
+    const uint32_t e = (uint32_t)p.src[r];
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
     w[i] = 0.0f;
-    if (e >= 0 && e < entries) {
+    if (e < entries) {
       live |= 1u << i;
-      a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / p.topk) * p.ld_dy + col0 + c0);
+      a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / (uint32_t)p.topk) * p.ld_dy + col0 + c0);
       b[i] = *reinterpret_cast<const uint4*>(p.d + r * p.ld_d + col0 + c0);
       w[i] = p.weights[e];
     }
@@ -244,26 +247,38 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
     dot = row_sum(dot);
     mine = i16 == i ? dot : mine;
   }
-  if (i16 < 8 && ((live >> i16) & 1)) p.dots[(row0 + r0 + i16) * (p.cols / kBlockK) + blockIdx.y] = mine;
-  tile_rows<8>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + blockIdx.y * p.ld_dsf + row0, live);
+  if (i16 < 8 && ((live >> i16) & 1)) p.dots[tile.col * (int64_t)p.m_total + row0 + r0 + i16] = mine;
+  tile_rows<8>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + tile.col * p.ld_dsf + row0, live);
   if (!p.dqt) return;
-  if (!__syncthreads_or(live != 0)) return;
-  tile_columns<8>(v, lds, p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total,
-                  p.dsft + (int64_t)blockIdx.x * p.ld_dsft + col0);
+  const ColumnsTo to[1] = {{p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, p.dsft + (int64_t)tile.row * p.ld_dsft + col0}};
+  tile_columns(vs, lds, to);
 }
 
-// dweights of each entry: 16 lanes add the dot products of its row's tiles.
+// Workgroup x: the dot products of rows [64 x, 64 x + 64), each wave every fourth
+// tile's, added into the rows' entries; and zeros for those of entries
+// [256 x, 256 x + 256) that no row is of.
 __global__ __launch_bounds__(256) void combine_dweights_kernel(CombineBwdParams p) {
-  const int64_t i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  __shared__ float part[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t entries = (int64_t)p.tokens * p.topk;
-  if (i >= entries) return;
-  const int r = p.rows[i], tiles = p.cols / kBlockK, sub = threadIdx.x & 15;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = (int64_t)blockIdx.x * 64 + lane;
+  if (i < entries) {
+    const int at = p.rows[i];
+    if (at < 0 || at >= p.m_total || p.src[at] != i) p.dweights[i] = 0.0f;
+  }
   float sum = 0.0f;
-  if (r >= 0 && r < p.m_total && p.src[r] == i)
-    for (int j = sub; j < tiles; j += 16) sum += p.dots[(int64_t)r * tiles + j];
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 16);
-  if (sub == 0) p.dweights[i] = sum;
+  int e = -1;
+  if (r < p.m_total) {
+    e = p.src[r];
+    if (e >= entries || (e >= 0 && p.rows[e] != r)) e = -1;
+  }
+  if (e >= 0) {
+#pragma unroll 4
+    for (int j = wave; j < p.cols / kBlockK; j += 4) sum += p.dots[j * (int64_t)p.m_total + r];
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && e >= 0) p.dweights[e] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
 }
 
 int plan_blocks(int64_t entries) {
@@ -312,10 +327,11 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream) {
-  if (p.m_total > 0)
-    hipLaunchKernelGGL(combine_bwd_kernel, dim3(p.m_total / kBlockK, p.cols / kBlockK), dim3(kTileThreads<8>), 0, stream, p);
+  const int tiles = p.m_total / kBlockK * (p.cols / kBlockK);
+  if (tiles > 0) hipLaunchKernelGGL(combine_bwd_kernel, dim3(tiles), dim3(kTileThreads<8>), 0, stream, p);
   const int64_t entries = (int64_t)p.tokens * p.topk;
-  hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)((entries + 15) / 16)), dim3(256), 0, stream, p);
+  const int64_t by_entry = (entries + 255) / 256, by_row = (p.m_total + 63) / 64;
+  hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)(by_entry > by_row ? by_entry : by_row)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

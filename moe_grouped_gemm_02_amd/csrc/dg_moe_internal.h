@@ -77,7 +77,7 @@ struct CombineBwdParams {
   uint8_t* dqt;  // null: no transposed codes
   float* dsft;
   float* dweights;
-  float* dots;  // [m_total][cols / 128] partial sums of the weights' gradient
+  float* dots;  // [cols / 128][m_total] partial sums of the weights' gradient
   int tokens, topk, cols, m_total;
   int64_t ld_dy, ld_d, ld_dsf, ld_dsft;
 };
