@@ -165,17 +165,25 @@ __global__ __launch_bounds__(kTileThreads<4>, 2) void swiglu_bwd_kernel(SwigluBw
   while (t < end) {
     const TileAt tile = {t % row_tiles, t / row_tiles};
     const uint32_t live = use.of_thread<4>();
+    if (__ballot(live != 15u)) {  // rows not in use count as zeros, whatever they hold
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = (live >> i) & 1;
+        raw.gate[i].x = in ? raw.gate[i].x : 0u, raw.gate[i].y = in ? raw.gate[i].y : 0u;
+        raw.up[i].x = in ? raw.up[i].x : 0u, raw.up[i].y = in ? raw.up[i].y : 0u;
+        raw.da[i].x = in ? raw.da[i].x : 0u, raw.da[i].y = in ? raw.da[i].y : 0u;
+        raw.da[i].z = in ? raw.da[i].z : 0u, raw.da[i].w = in ? raw.da[i].w : 0u;
+        raw.gate_s[i] = in ? raw.gate_s[i] : 0.0f, raw.up_s[i] = in ? raw.up_s[i] : 0.0f;
+      }
+    }
     float out[3][4][8];  // d gate, d up, and the unit's output
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = (live >> i) & 1;
-      const uint2 none = make_uint2(0, 0);
       float gate[8], up[8];
-      decode8(in ? raw.gate[i] : none, gate);
-      decode8(in ? raw.up[i] : none, up);
-      const float gate_s = in ? raw.gate_s[i] : 0.0f, up_s = in ? raw.up_s[i] : 0.0f;
-      const uint4 d = raw.da[i];
-      const uint32_t b[4] = {in ? d.x : 0u, in ? d.y : 0u, in ? d.z : 0u, in ? d.w : 0u};
+      decode8(raw.gate[i], gate);
+      decode8(raw.up[i], up);
+      const float gate_s = raw.gate_s[i], up_s = raw.up_s[i];
+      const uint32_t b[4] = {raw.da[i].x, raw.da[i].y, raw.da[i].z, raw.da[i].w};
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const float da = bf16_bits_to_f32((c & 1) ? b[c >> 1] >> 16 : b[c >> 1] & 0xFFFFu);
