@@ -9,37 +9,6 @@
 namespace dg {
 namespace {
 
-// Sixteen bf16 values of a lane, widened.
-struct Lane16 {
-  uint32_t w[8];
-  __device__ __forceinline__ float at(int i) const {
-    return bf16_bits_to_f32((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-  }
-};
-__device__ __forceinline__ Lane16 load16(const uint16_t* p) {
-  const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 8);
-  return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-}
-
-// The 1x128 code of a bf16 tile whose 16 values a lane are in v, as the plain
-// activation quantiser computes it.
-__device__ __forceinline__ void store_bf16_tile(const Lane16& v, uint8_t* q, float* sf, int sub) {
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v.at(i)));
-#pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 8));
-  const float s = amax / 448.0f;
-  const double rcp = tile_reciprocal(s);
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    out[i] = e4m3_x4(quotient(v.w[2 * i] & 0xFFFFu, rcp), quotient(v.w[2 * i] >> 16, rcp),
-                     quotient(v.w[2 * i + 1] & 0xFFFFu, rcp), quotient(v.w[2 * i + 1] >> 16, rcp));
-  *reinterpret_cast<uint4*>(q) = make_uint4(out[0], out[1], out[2], out[3]);
-  if (sub == 0) *sf = s;
-}
-
 constexpr int kTilesPerWave = 8;
 constexpr int kRowWaves = 4;
 
@@ -61,38 +30,33 @@ __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) 
     const int col = j * kBlockK + sub * 16;
     const uint16_t* h = p.h + gr * p.ld_h + col;
     const Lane16 gate = load16(h), up = load16(h + p.inter);
-    float a[16], amax = 0.0f;
+    float a[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float v = gate.at(i);
       a[i] = v * sigmoid(v).sig * up.at(i);
-      amax = fmaxf(amax, fabsf(a[i]));
     }
-#pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 8));
-    uint32_t out[4];
+    const float amax = amax16([&](int i) { return a[i]; });
+    uint4 out;
     const int64_t sf_at = (g * tiles + j) * p.ld_sf + r;
     if constexpr (POW2) {
       const uint32_t e = ue8m0_exponent_f32(amax);
       const int up2 = 127 - (int)e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[i] = e4m3_x4(__builtin_ldexpf(a[4 * i], up2), __builtin_ldexpf(a[4 * i + 1], up2),
-                         __builtin_ldexpf(a[4 * i + 2], up2), __builtin_ldexpf(a[4 * i + 3], up2));
+      out = encode16([&](int i) { return __builtin_ldexpf(a[i], up2); });
       if (sub == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
     } else {
       const TileScale t = tile_scale(amax);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[i] = e4m3_x4(a[4 * i] * t.inv, a[4 * i + 1] * t.inv, a[4 * i + 2] * t.inv, a[4 * i + 3] * t.inv);
+      out = encode16([&](int i) { return a[i] * t.inv; });
       if (sub == 0) static_cast<float*>(p.sf)[sf_at] = t.s;
     }
-    *reinterpret_cast<uint4*>(p.q + gr * p.inter + col) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(p.q + gr * p.inter + col) = out;
     if constexpr (CKPT) {
       uint8_t* hq = p.hq + gr * 2 * p.inter + col;
       float* hsf = p.hsf + (g * 2 * tiles + j) * p.ld_hsf + r;
-      store_bf16_tile(gate, hq, hsf, sub);
-      store_bf16_tile(up, hq + p.inter, hsf + (int64_t)tiles * p.ld_hsf, sub);
+      float gs, us;
+      *reinterpret_cast<uint4*>(hq) = encode_bf16_tile(gate, gs);
+      *reinterpret_cast<uint4*>(hq + p.inter) = encode_bf16_tile(up, us);
+      if (sub == 0) hsf[0] = gs, hsf[tiles * p.ld_hsf] = us;
     }
   }
 }

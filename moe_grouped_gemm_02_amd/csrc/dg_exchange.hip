@@ -11,98 +11,148 @@ namespace {
 
 // ------------------------------------------------------------------- plan --
 
+// A stable counting sort.  Blocks of 1024 entries count their experts (one
+// launch) and place their entries (another): the rank of an entry is the count
+// of its expert in the blocks before, in the waves before, and in the lanes
+// before, which a ballot for each bit of the expert's number tells.  Up to 4096
+// entries one workgroup does it all in one launch (1024 entries of 32 experts:
+// 4.7 us, against 1.3 + 4.7 in two launches).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kOnePlanEntries = 4096;
+constexpr int kOnePlanRows = 1 << 15;  // what one workgroup can fill in about as long as it sorts
+
+int plan_blocks(int64_t entries) {
+  const int64_t b = (entries + kPlanThreads - 1) / kPlanThreads;
+  return (int)(b > 0 ? b : 1);
+}
 
 // Local expert of an entry, or -1.
-__device__ __forceinline__ int local_of(int id, const PlanParams& p) {
+__device__ __forceinline__ int local_of(int64_t i, const PlanParams& p) {
+  const int id = i < p.entries ? p.ids[i] : -1;
   const int64_t g = (int64_t)id - p.first;
-  return g >= 0 && g < p.groups && id >= 0 ? (int)g : -1;
+  return id >= 0 && g >= 0 && g < p.groups ? (int)g : -1;
 }
 
 // Counts the experts of each block's 1024 entries.
 __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) {
   __shared__ int count[kMaxLocalExperts];
-  for (int g = threadIdx.x; g < p.groups; g += kPlanThreads) count[g] = 0;
+  const int tid = threadIdx.x;
+  const int g = local_of((int64_t)blockIdx.x * kPlanThreads + tid, p);
+  if (tid < p.groups) count[tid] = 0;
   __syncthreads();
-  const int64_t i = (int64_t)blockIdx.x * kPlanThreads + threadIdx.x;
-  const int g = i < p.entries ? local_of(p.ids[i], p) : -1;
   if (g >= 0) atomicAdd(&count[g], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.groups; e += kPlanThreads) p.hist[(int64_t)blockIdx.x * p.groups + e] = count[e];
+  if (tid < p.groups) p.hist[(int64_t)blockIdx.x * p.groups + tid] = count[tid];
 }
 
-// Places each block's 1024 entries and fills the index arrays of its share of
-// the layout's rows.
+// Places the entries and fills the index arrays of the layout's rows.  ONE: one
+// workgroup, which counts the entries itself; otherwise block b places entries
+// [1024 b, 1024 b + 1024) with the counts of all blocks.
+template <bool ONE>
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) {
   __shared__ int start[kMaxLocalExperts + 1];  // first row of each group
   __shared__ int count[kMaxLocalExperts];      // entries of each group
-  __shared__ int base[kMaxLocalExperts];       // entries of each group before this block
+  __shared__ int base[kMaxLocalExperts];       // of them, those placed before
   __shared__ uint16_t per_wave[kPlanWaves][kMaxLocalExperts];
+  __shared__ uint32_t totals[kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int g = tid; g < p.groups; g += kPlanThreads) {
-    int before = 0, all = 0;
-    for (int b = 0; b < (int)gridDim.x; ++b) {
-      if (b == (int)blockIdx.x) before = all;
-      all += p.hist[(int64_t)b * p.groups + g];
-    }
-    count[g] = all;
-    base[g] = before;
-  }
-  for (int i = tid; i < kPlanWaves * p.groups; i += kPlanThreads) per_wave[i / p.groups][i % p.groups] = 0;
+  const int first_chunk = ONE ? 0 : blockIdx.x, chunks = ONE ? (p.entries + kPlanThreads - 1) / kPlanThreads : blockIdx.x + 1;
+  int g = local_of((int64_t)first_chunk * kPlanThreads + tid, p);
+  if (tid < p.groups) count[tid] = base[tid] = 0;
   __syncthreads();
-  if (tid == 0) {
-    int64_t at = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      start[g] = (int)(at < p.layout_rows ? at : p.layout_rows);
-      at += p.masked ? p.m_max : ((int64_t)count[g] + kBlockK - 1) / kBlockK * kBlockK;
+  if constexpr (ONE) {
+    if (g >= 0) atomicAdd(&count[g], 1);
+    for (int c = 1; c < chunks; ++c) {
+      const int e = local_of((int64_t)c * kPlanThreads + tid, p);
+      if (e >= 0) atomicAdd(&count[e], 1);
     }
-    start[p.groups] = (int)(at < p.layout_rows ? at : p.layout_rows);
+  } else {
+    const int before = blockIdx.x * p.groups, all = gridDim.x * p.groups;
+    for (int i = tid; i < all; i += kPlanThreads) {
+      const int v = p.hist[i], e = i % p.groups;
+      atomicAdd(&count[e], v);
+      if (i < before) atomicAdd(&base[e], v);
+    }
+  }
+  __syncthreads();
+  // Starts of the groups: exclusive sums of their sizes.
+  {
+    uint32_t size = 0;
+    if (tid < p.groups) size = p.masked ? p.m_max : (uint32_t)(count[tid] + kBlockK - 1) / kBlockK * kBlockK;
+    uint32_t sum = size;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t other = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += other;
+    }
+    if (lane == 63) totals[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) sum += totals[w];
+    const uint32_t limit = (uint32_t)p.layout_rows;
+    if (tid < p.groups) {
+      start[tid] = (int)umin(sum - size, limit);
+      if (tid == p.groups - 1) start[p.groups] = (int)umin(sum, limit);
+    }
+    __syncthreads();
   }
 
-  const int64_t i = (int64_t)blockIdx.x * kPlanThreads + tid;
-  const int g = i < p.entries ? local_of(p.ids[i], p) : -1;
-  // Lanes of this wave with the same expert.
-  uint64_t same = __ballot(g >= 0);
-  for (int bit = 1; bit < p.groups; bit <<= 1) {
-    const uint64_t ones = __ballot(g & bit);
-    same &= (g & bit) ? ones : ~ones;
-  }
-  const int ahead = __popcll(same & ((1ull << lane) - 1ull));
-  if (g >= 0 && ahead == 0) per_wave[wave][g] = (uint16_t)__popcll(same);
-  __syncthreads();
-  if (i < p.entries) {
-    int row = -1;
-    if (g >= 0) {
-      int rank = base[g] + ahead;
-      for (int w = 0; w < wave; ++w) rank += per_wave[w][g];
-      const int64_t at = (int64_t)start[g] + rank;
-      const int64_t end = p.masked ? (int64_t)start[g] + p.m_max : p.layout_rows;
-      if (at < end) {
-        row = (int)at;
-        p.src[row] = (int)i;
+  for (int c = first_chunk; c < chunks; ++c) {
+    const int64_t i = (int64_t)c * kPlanThreads + tid;
+    if (c != first_chunk) g = local_of(i, p);
+    for (int k = tid; k < kPlanWaves * p.groups; k += kPlanThreads) per_wave[k / p.groups][k % p.groups] = 0;
+    // Lanes of this wave with the same expert.
+    uint64_t same = __ballot(g >= 0);
+    for (int bit = 1; bit < p.groups; bit <<= 1) {
+      const uint64_t ones = __ballot(g & bit);
+      same &= (g & bit) ? ones : ~ones;
+    }
+    const int ahead = __popcll(same & ((1ull << lane) - 1ull));
+    __syncthreads();
+    if (g >= 0 && ahead == 0) per_wave[wave][g] = (uint16_t)__popcll(same);
+    __syncthreads();
+    if (i < p.entries) {
+      int row = -1;
+      if (g >= 0) {
+        int rank = base[g] + ahead;
+#pragma unroll
+        for (int w = 0; w < kPlanWaves; ++w) rank += w < wave ? per_wave[w][g] : 0;
+        const int64_t at = (int64_t)start[g] + rank;
+        if (at < (p.masked ? (int64_t)start[g] + p.m_max : p.layout_rows)) {
+          row = (int)at;
+          p.src[row] = (int)i;
+        }
       }
+      p.rows[i] = row;
     }
-    p.rows[i] = row;
+    if (ONE && c + 1 < chunks) {
+      __syncthreads();
+      if (tid < p.groups)
+        for (int w = 0; w < kPlanWaves; ++w) base[tid] += per_wave[w][tid];
+      __syncthreads();
+    }
   }
 
-  const int64_t all_threads = (int64_t)gridDim.x * kPlanThreads;
-  for (int64_t r = i; r < p.layout_rows; r += all_threads) {
-    int lo = 0, hi = p.groups;  // the last group that starts at or before row r and holds rows
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (start[mid] <= r) lo = mid;
-      else hi = mid;
+  for (int64_t r = (int64_t)blockIdx.x * kPlanThreads + tid; r < p.layout_rows; r += (int64_t)gridDim.x * kPlanThreads) {
+    int lo = 0;  // the last group that starts at or before row r
+    if (p.masked) {
+      lo = (int)((uint32_t)r / (uint32_t)p.m_max);
+    } else {
+      int hi = p.groups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (start[mid] <= r) lo = mid;
+        else hi = mid;
+      }
     }
     const bool used = r - start[lo] < count[lo];
     if (!used) p.src[r] = -1;
     if (p.m_indices) p.m_indices[r] = used ? lo : -1;
   }
   if (blockIdx.x == 0) {
-    for (int e = tid; e <= p.groups; e += kPlanThreads) {
-      if (p.k_offsets) p.k_offsets[e] = start[e];
-      if (p.masked_m && e < p.groups) p.masked_m[e] = count[e] < p.m_max ? count[e] : p.m_max;
-    }
+    if (p.k_offsets)
+      for (int e = tid; e <= p.groups; e += kPlanThreads) p.k_offsets[e] = start[e];
+    if (p.masked_m && tid < p.groups) p.masked_m[tid] = count[tid] < p.m_max ? count[tid] : p.m_max;
   }
 }
 
@@ -118,57 +168,37 @@ template <bool POW2, int U>
 __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams p) {
   const int tiles_per_row = p.cols / kBlockK;
   const int64_t total_rows = (int64_t)p.groups * p.rows;
-  const int64_t entries = (int64_t)p.tokens * p.topk;
+  const uint32_t entries = (uint32_t)(p.tokens * p.topk);
   const int sub = threadIdx.x & 7;
   const int j = blockIdx.x * kTilesPerWave + ((threadIdx.x & 63) >> 3);
   const int wave = threadIdx.x >> 6;
   if (j >= tiles_per_row) return;
   const int64_t step = (int64_t)gridDim.y * kRowWaves * U;
   for (int64_t r0 = ((int64_t)blockIdx.y * kRowWaves + wave) * U; r0 < total_rows; r0 += step) {
-    uint4 lo[U], hi[U];
+    Lane16 in[U];
     bool live[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int e = r0 + u < total_rows ? p.src[r0 + u] : -1;
-      live[u] = e >= 0 && e < entries;
-      lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-      if (live[u]) {
-        const uint16_t* from = p.x + (int64_t)(e / p.topk) * p.ld_x + j * kBlockK + sub * 16;
-        lo[u] = *reinterpret_cast<const uint4*>(from);
-        hi[u] = *reinterpret_cast<const uint4*>(from + 8);
-      }
+      const uint32_t e = r0 + u < total_rows ? (uint32_t)p.src[r0 + u] : ~0u;
+      live[u] = e < entries;
+      if (live[u]) in[u] = load16(p.x + (int64_t)(e / (uint32_t)p.topk) * p.ld_x + j * kBlockK + sub * 16);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!live[u]) continue;
       const int64_t gr = r0 + u;
       const int64_t g = gr / p.rows, r = gr - g * p.rows;
-      const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_bits_to_f32(w[i] & 0xFFFFu)), fabsf(bf16_bits_to_f32(w[i] >> 16))));
-#pragma unroll
-      for (int off = 4; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 8));
-      uint32_t out[4];
       const int64_t sf_at = (g * tiles_per_row + j) * p.ld_sf + r;
+      uint4* to = reinterpret_cast<uint4*>(p.q + gr * p.cols + j * kBlockK + sub * 16);
       if constexpr (POW2) {
-        const uint32_t e = ue8m0_exponent(amax);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          out[i] = e4m3_x4(pow2_quotient(w[2 * i] & 0xFFFFu, e), pow2_quotient(w[2 * i] >> 16, e),
-                           pow2_quotient(w[2 * i + 1] & 0xFFFFu, e), pow2_quotient(w[2 * i + 1] >> 16, e));
+        uint32_t e;
+        *to = encode_bf16_tile_pow2(in[u], e);
         if (sub == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
       } else {
-        const float s = amax / 448.0f;
-        const double rcp = tile_reciprocal(s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          out[i] = e4m3_x4(quotient(w[2 * i] & 0xFFFFu, rcp), quotient(w[2 * i] >> 16, rcp),
-                           quotient(w[2 * i + 1] & 0xFFFFu, rcp), quotient(w[2 * i + 1] >> 16, rcp));
+        float s;
+        *to = encode_bf16_tile(in[u], s);
         if (sub == 0) static_cast<float*>(p.sf)[sf_at] = s;
       }
-      *reinterpret_cast<uint4*>(p.q + gr * p.cols + j * kBlockK + sub * 16) = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
@@ -281,11 +311,6 @@ __global__ __launch_bounds__(256) void combine_dweights_kernel(CombineBwdParams 
   if (wave == 0 && e >= 0) p.dweights[e] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
 }
 
-int plan_blocks(int64_t entries) {
-  const int64_t b = (entries + kPlanThreads - 1) / kPlanThreads;
-  return (int)(b > 0 ? b : 1);
-}
-
 }  // namespace
 
 size_t plan_workspace_bytes(int64_t entries, int groups) {
@@ -294,8 +319,12 @@ size_t plan_workspace_bytes(int64_t entries, int groups) {
 
 hipError_t launch_plan(const PlanParams& p, hipStream_t stream) {
   const dim3 grid(plan_blocks(p.entries)), block(kPlanThreads);
-  hipLaunchKernelGGL(plan_count_kernel, grid, block, 0, stream, p);
-  hipLaunchKernelGGL(plan_place_kernel, grid, block, 0, stream, p);
+  if (p.entries <= kOnePlanEntries && p.layout_rows <= kOnePlanRows) {
+    hipLaunchKernelGGL(plan_place_kernel<true>, dim3(1), block, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL(plan_count_kernel, grid, block, 0, stream, p);
+    hipLaunchKernelGGL(plan_place_kernel<false>, grid, block, 0, stream, p);
+  }
   return hipGetLastError();
 }
 
@@ -306,7 +335,7 @@ hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t strea
   int64_t gy = (16384 / kRowWaves + gx - 1) / gx;
   const int64_t need = (total + kRowWaves * u - 1) / (kRowWaves * u);
   if (gy > need) gy = need;
-  const dim3 grid(gx, (unsigned)(gy < 1 ? 1 : gy > 65535 ? 65535 : gy)), block(64 * kRowWaves);
+  const dim3 grid(gx, (unsigned)(gy < 1 ? 1 : gy)), block(64 * kRowWaves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
   if (pow2) {
     if (u == 4) go(dispatch_kernel<true, 4>);

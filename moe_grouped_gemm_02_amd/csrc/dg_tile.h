@@ -44,6 +44,74 @@ __device__ __forceinline__ float silu_slope(float code, float scale, float v, co
   return s.sig * s.n * (fabsf(u) < 0.0625f ? near : far);
 }
 
+// Sixteen bf16 values of a lane; eight lanes own a tile of 128.
+struct Lane16 {
+  uint32_t w[8];
+  __device__ __forceinline__ float at(int i) const {
+    return (i & 1) ? __uint_as_float(w[i >> 1] & 0xFFFF0000u) : __uint_as_float(w[i >> 1] << 16);
+  }
+};
+__device__ __forceinline__ Lane16 load16(const uint16_t* p) {
+  const uint4 lo = *reinterpret_cast<const uint4*>(p), hi = *reinterpret_cast<const uint4*>(p + 8);
+  return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+}
+
+// Maximum over the eight lanes of a tile, of values that are not negative.
+__device__ __forceinline__ float max_of_tile(float v) {
+  uint32_t u = __float_as_uint(v);
+  u = umax(u, dpp<kXor1>(u));
+  u = umax(u, dpp<kXor2>(u));
+  u = umax(u, dpp<kHalfMirror>(u));
+  return __uint_as_float(u);
+}
+
+template <typename Values>
+__device__ __forceinline__ float amax16(const Values& at) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) m = fmaxf(m, fmaxf(fabsf(at(i)), fabsf(at(i + 1))));
+  return max_of_tile(m);
+}
+
+template <typename Values>
+__device__ __forceinline__ uint4 encode16(const Values& at) {
+  return make_uint4(e4m3_x4(at(0), at(1), at(2), at(3)), e4m3_x4(at(4), at(5), at(6), at(7)),
+                    e4m3_x4(at(8), at(9), at(10), at(11)), e4m3_x4(at(12), at(13), at(14), at(15)));
+}
+
+// Codes and scale of a bf16 tile, those of the plain activation quantiser bit
+// for bit: s = fp32(amax / 448), q = e4m3(fp32(x / s)).  Both quotients are a
+// product with the rounded reciprocal and one correction by the exact residual,
+// which is the rounded quotient itself (all s and |x| <= amax of normal bf16
+// magnitude tried on the host, 1.03e9 pairs; quotients below 2^-12 may differ
+// and have the code of zero).  The residual's order keeps the sign of a zero.
+// That needs residuals that float32 holds: tiles with s below 2^-90 (an all-zero
+// one among them) take the double-precision form.  (The latter for all: dispatch
+// of 32768 x 7168 131 us.)
+__device__ __forceinline__ uint4 encode_bf16_tile(const Lane16& v, float& s) {
+  const float amax = amax16([&](int i) { return v.at(i); });
+  constexpr float kInv448 = 1.0f / 448.0f;
+  const float s0 = amax * kInv448;
+  s = fmaf(fmaf(-448.0f, s0, amax), kInv448, s0);
+  if (__ballot(!(s >= 0x1p-90f))) {
+    s = amax / 448.0f;
+    const double rcp = tile_reciprocal(s);
+    return encode16([&](int i) { return (float)((double)v.at(i) * rcp); });
+  }
+  float inv = reciprocal(s);
+  inv = fmaf(fmaf(-s, inv, 1.0f), inv, inv);
+  return encode16([&](int i) {
+    const float x = v.at(i), q = x * inv;
+    return fmaf(-fmaf(s, q, -x), inv, q);
+  });
+}
+// The same with a power-of-two scale 2^(e - 127).
+__device__ __forceinline__ uint4 encode_bf16_tile_pow2(const Lane16& v, uint32_t& e) {
+  e = ue8m0_exponent_f32(amax16([&](int i) { return v.at(i); }));
+  const int up = 127 - (int)e;
+  return encode16([&](int i) { return __builtin_ldexpf(v.at(i), up); });
+}
+
 // 128 x 128 tiles.  Thread t of the workgroup holds R rows, R (t / 16) on, and
 // 8 columns, 8 (t % 16) on: a row of the tile is 16 lanes, a row of the
 // hardware's row operations, and the R rows of a column are R bytes of the

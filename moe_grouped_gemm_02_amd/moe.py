@@ -91,6 +91,10 @@ def _topk(t, name, tokens):
 
 def _rows_of(t, name, dtypes, ndim=2):
     """A matrix with unit stride in its rows; returns its row stride."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes:
+        stride = t.stride()
+        if len(stride) == ndim and stride[-1] == 1 and t.shape[-2] > 1 and t.numel():
+            return stride[-2]
     _expect(t, name, dtypes, ndim)
     if t.shape[-2] <= 1 or t.numel() == 0:  # such strides say nothing
         if t.shape[-1] > 1 and t.numel():
@@ -102,6 +106,10 @@ def _rows_of(t, name, dtypes, ndim=2):
 
 def _scales(t, name, dtypes, lead, rows):
     """A contiguous scale matrix [*lead][ld] with ld >= rows; returns ld."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
+        shape = t.shape
+        if shape[:-1] == lead and shape[-1] >= rows:
+            return shape[-1]
     _expect(t, name, dtypes, len(lead) + 1)
     _shape(t, name, (*lead, t.shape[-1]))
     if t.shape[-1] < rows:
@@ -176,11 +184,21 @@ def dg_moe_route_bwd_bf16(logits, ids, dweights, dlogits, score="softmax", renor
 
 # --------------------------------------------------------------- exchange --
 
+def _vector(t, name):
+    """Length of a contiguous vector of indices."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous()):
+        _expect(t, name, _I32, 1)
+        _contig(t, name)
+    return t.shape[0]
+
+
 def _entries(ids, rows):
-    _expect(ids, "ids", _I32, 2)
-    _contig(ids, "ids")
-    _dense(rows, "rows", _I32, ids.shape)
-    return ids.shape
+    if type(ids) is not torch.Tensor or ids.dim() != 2:
+        _expect(ids, "ids", _I32, 2)
+    shape = ids.shape
+    _dense(ids, "ids", _I32, shape)
+    _dense(rows, "rows", _I32, shape)
+    return shape
 
 
 def dg_get_moe_plan_workspace_size(tokens, topk, num_groups):
@@ -192,42 +210,38 @@ def dg_moe_plan_contiguous(ids, rows, src, m_indices, k_offsets, first_expert=0,
     layout row src (entry t * k + j or -1) and m_indices (group or -1), and
     k_offsets [G+1], all int32.  Group g is expert first_expert + g."""
     tokens, topk = _entries(ids, rows)
-    _expect(src, "src", _I32, 1)
-    m_total = src.shape[0]
-    _contig(src, "src")
+    m_total = _vector(src, "src")
     _dense(m_indices, "m_indices", _I32, (m_total,))
-    _expect(k_offsets, "k_offsets", _I32, 1)
-    _contig(k_offsets, "k_offsets")
+    groups = _vector(k_offsets, "k_offsets") - 1
     _call("dg_moe_plan_contiguous", _ptr(ids), _ptr(rows), _ptr(src), _ptr(m_indices), _ptr(k_offsets), tokens, topk,
-          int(first_expert), k_offsets.shape[0] - 1, m_total, _ptr(workspace), _ws(workspace), _stream(ids))
+          int(first_expert), groups, m_total, _ptr(workspace), _ws(workspace), _stream(ids))
     return rows, src, m_indices, k_offsets
 
 
 def dg_moe_plan_masked(ids, rows, src, masked_m, first_expert=0, workspace=None):
     """Row plan of the masked layout: src holds G * M_max entries, masked_m [G]."""
     tokens, topk = _entries(ids, rows)
-    _expect(masked_m, "masked_m", _I32, 1)
-    _contig(masked_m, "masked_m")
-    _expect(src, "src", _I32, 1)
-    _contig(src, "src")
-    groups = masked_m.shape[0]
-    if groups < 1 or src.shape[0] % groups:
+    groups, layout_rows = _vector(masked_m, "masked_m"), _vector(src, "src")
+    if groups < 1 or layout_rows % groups:
         raise ValueError("src must hold the same number of rows for every group")
     _call("dg_moe_plan_masked", _ptr(ids), _ptr(rows), _ptr(src), _ptr(masked_m), tokens, topk, int(first_expert),
-          groups, src.shape[0] // groups, _ptr(workspace), _ws(workspace), _stream(ids))
+          groups, layout_rows // groups, _ptr(workspace), _ws(workspace), _stream(ids))
     return rows, src, masked_m
 
 
 def _codes(q, sf, sf_dtypes):
     """(groups, rows, cols, ld) of codes [(G)][rows][cols] and scales [(G)][cols/128][ld]."""
-    _expect(q, "q", _U8)
-    if q.dim() not in (2, 3):
-        raise ValueError("q must have 2 or 3 dimensions")
-    _contig(q, "q")
-    groups = q.shape[0] if q.dim() == 3 else 1
-    rows, cols = q.shape[-2:]
-    ld = _scales(sf, "sf", sf_dtypes, (*q.shape[:-2], cols // 128), rows)
-    return groups, rows, cols, ld
+    if not (type(q) is torch.Tensor and q.is_cuda and q.dtype in _U8 and q.is_contiguous()):
+        _expect(q, "q", _U8)
+        _contig(q, "q")
+    shape = q.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        return 1, rows, cols, _scales(sf, "sf", sf_dtypes, (cols // 128,), rows)
+    if len(shape) == 3:
+        groups, rows, cols = shape
+        return groups, rows, cols, _scales(sf, "sf", sf_dtypes, (groups, cols // 128), rows)
+    raise ValueError("q must have 2 or 3 dimensions")
 
 
 def _dispatch(fn, sf_dtypes, x, src, q, sf, topk):
@@ -303,8 +317,9 @@ def dg_moe_combine_bwd(dy, d, src, rows, weights, dq, dsf, dqt, dsft, dweights, 
 def _swiglu_args(h, q, sf, sf_dtypes, m_indices, masked_m):
     groups, rows, inter, ld_sf = _codes(q, sf, sf_dtypes)
     ld_h = _rows_of(h, "h", _BF, q.dim())
-    _shape(h, "h", (*q.shape[:-1], 2 * inter))
-    if h.dim() == 3 and groups > 1 and h.stride(0) != rows * ld_h:
+    if h.shape != ((rows, 2 * inter) if q.dim() == 2 else (groups, rows, 2 * inter)):
+        _shape(h, "h", (*q.shape[:-1], 2 * inter))
+    if groups > 1 and h.stride(0) != rows * ld_h:
         raise ValueError("h must have its groups one after another")
     if m_indices is not None:
         _dense(m_indices, "m_indices", _I32, (rows,))

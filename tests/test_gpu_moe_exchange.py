@@ -130,6 +130,25 @@ def test_dispatch(ue, tokens, topk, cols, groups, rows, pad, ld):
         assert np.all(sf[g][:, rows:] == (0x5A if ue else -3.0))
 
 
+def test_dispatch_every_tile_maximum():
+    """One tile for every positive finite bf16 as its largest magnitude, the
+    others below it in magnitude, zeros of both signs among them."""
+    dg = require_gpu()
+    amax = np.arange(1, 0x7F80, dtype=np.uint16)
+    rng = np.random.default_rng(3)
+    x = (rng.random((amax.size, 128)) * (amax[:, None] + 1)).astype(np.uint16)
+    near = rng.random(x.shape) < 0.5  # half of them in the few binades that do not become zero
+    x = np.where(near, np.maximum(amax[:, None].astype(np.int64) - rng.integers(0, 1800, x.shape), 0).astype(np.uint16), x)
+    x |= (rng.integers(0, 2, x.shape) << 15).astype(np.uint16)
+    x[:, 0] = amax
+    x[:, 1], x[:, 2] = 0x0000, 0x8000
+    for ue in (False, True):
+        q, sf = _dispatch(dg, x, np.arange(amax.size, dtype=np.int32), 1, 1, amax.size, ue)
+        ref_q, ref_sf = (ue8m0.quant_1x128_ue8m0 if ue else quant.quant_1x128)(x)
+        assert np.array_equal(sf[0][:, :amax.size], ref_sf[:, :amax.size])
+        assert np.array_equal(q[0], ref_q)
+
+
 @pytest.mark.parametrize("weighted", [True, False])
 @pytest.mark.parametrize("tokens,topk,cols,total,pad", [
     (1, 1, 8, 1, 0), (3, 2, 136, 5, 8), (100, 8, 2048, 300, 0), (65, 32, 2056, 64, 16), (40, 6, 7168, 0, 0), (513, 3, 4104, 999, 0)])
