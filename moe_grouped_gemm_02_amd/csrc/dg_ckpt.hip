@@ -13,20 +13,20 @@ constexpr int kTilesPerWave = 8;
 constexpr int kRowWaves = 4;
 
 // 8 lanes own one 128-value tile of a row's gate and the same tile of its up
-// half; a wave owns 8 tiles, block (x, y) tiles [8 x, 8 x + 8) and four rows at a
-// time.
-template <bool POW2, bool CKPT>
+// half; a wave owns 8 tiles.  Block (x, y, g): tiles [8 x, 8 x + 8) of group g,
+// row 4 y + its wave and every 4 gridDim.y rows on, up to the group's last row in
+// use.  STREAMING: results larger than the L2s.
+template <bool POW2, bool CKPT, bool STREAMING>
 __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) {
   const int tiles = p.inter / kBlockK;
   const int sub = threadIdx.x & 7;
   const int j = blockIdx.x * kTilesPerWave + ((threadIdx.x & 63) >> 3);
   if (j >= tiles) return;
-  const int64_t total = (int64_t)p.groups * p.rows;
-  for (int64_t gr = (int64_t)blockIdx.y * kRowWaves + (threadIdx.x >> 6); gr < total;
-       gr += (int64_t)gridDim.y * kRowWaves) {
-    const int64_t g = gr / p.rows, r = gr - g * p.rows;
-    if (p.m_indices && p.m_indices[gr] < 0) continue;
-    if (p.masked_m && r >= p.masked_m[g]) continue;
+  const int64_t g = blockIdx.z;
+  const int rows = p.masked_m ? min(p.masked_m[g], p.rows) : p.rows;
+  for (int r = blockIdx.y * kRowWaves + (threadIdx.x >> 6); r < rows; r += gridDim.y * kRowWaves) {
+    if (p.m_indices && p.m_indices[r] < 0) continue;
+    const int64_t gr = g * p.rows + r;
     const int col = j * kBlockK + sub * 16;
     const uint16_t* h = p.h + gr * p.ld_h + col;
     const Lane16 gate = load16(h), up = load16(h + p.inter);
@@ -49,13 +49,13 @@ __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) 
       out = encode16([&](int i) { return a[i] * t.inv; });
       if (sub == 0) static_cast<float*>(p.sf)[sf_at] = t.s;
     }
-    *reinterpret_cast<uint4*>(p.q + gr * p.inter + col) = out;
+    store<STREAMING>(p.q + gr * p.inter + col, out);
     if constexpr (CKPT) {
       uint8_t* hq = p.hq + gr * 2 * p.inter + col;
       float* hsf = p.hsf + (g * 2 * tiles + j) * p.ld_hsf + r;
       float gs, us;
-      *reinterpret_cast<uint4*>(hq) = encode_bf16_tile(gate, gs);
-      *reinterpret_cast<uint4*>(hq + p.inter) = encode_bf16_tile(up, us);
+      store<STREAMING>(hq, encode_bf16_tile(gate, gs));
+      store<STREAMING>(hq + p.inter, encode_bf16_tile(up, us));
       if (sub == 0) hsf[0] = gs, hsf[tiles * p.ld_hsf] = us;
     }
   }
@@ -91,9 +91,9 @@ __device__ __forceinline__ void load_raw(const SwigluBwdParams& p, TileAt tile, 
   const uint16_t* dact = p.dact + row * p.ld_dact + col;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    raw.gate[i] = *reinterpret_cast<const uint2*>(hq + (int64_t)i * 2 * p.inter);
-    raw.up[i] = *reinterpret_cast<const uint2*>(hq + (int64_t)i * 2 * p.inter + p.inter);
-    raw.da[i] = *reinterpret_cast<const uint4*>(dact + i * p.ld_dact);
+    raw.gate[i] = load_streaming2(hq + (int64_t)i * 2 * p.inter);
+    raw.up[i] = load_streaming2(hq + (int64_t)i * 2 * p.inter + p.inter);
+    raw.da[i] = load_streaming4(dact + i * p.ld_dact);
   }
   load_floats<4>(p.hsf + tile.col * p.ld_hsf + row, raw.gate_s);
   load_floats<4>(p.hsf + (tiles + tile.col) * p.ld_hsf + row, raw.up_s);
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParam
   auto& v = vs[0];
   const uint8_t* from = p.q + (row0 + r0) * p.cols + col0 + c0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = *reinterpret_cast<const uint2*>(from + (int64_t)i * p.cols);
+  for (int i = 0; i < 8; ++i) q[i] = load_streaming2(from + (int64_t)i * p.cols);
   load_floats<8>(p.sf + tile.col * p.ld_sf + row0 + r0, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -209,14 +209,19 @@ __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParam
 
 hipError_t launch_swiglu_quant(const SwigluParams& p, bool pow2, hipStream_t stream) {
   const int gx = (p.inter / kBlockK + kTilesPerWave - 1) / kTilesPerWave;
-  const int64_t total = (int64_t)p.groups * p.rows;
-  int64_t gy = (16384 / kRowWaves + gx - 1) / gx;
-  const int64_t need = (total + kRowWaves - 1) / kRowWaves;
-  if (gy > need) gy = need;
-  const dim3 grid(gx, (unsigned)(gy < 1 ? 1 : gy > 65535 ? 65535 : gy)), block(64 * kRowWaves);
-  if (pow2) hipLaunchKernelGGL((swiglu_kernel<true, false>), grid, block, 0, stream, p);
-  else if (p.hq) hipLaunchKernelGGL((swiglu_kernel<false, true>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((swiglu_kernel<false, false>), grid, block, 0, stream, p);
+  // Up to 4096 workgroups in all; each group its share of them.
+  const int64_t share = (4096 + (int64_t)gx * p.groups - 1) / ((int64_t)gx * p.groups);
+  const int64_t need = ((int64_t)p.rows + kRowWaves - 1) / kRowWaves;
+  const dim3 grid(gx, (unsigned)(need < share ? need : share), p.groups), block(64 * kRowWaves);
+  const bool streaming = (int64_t)p.groups * p.rows * p.inter > (int64_t)32 << 20;
+  auto go = [&](auto pow, auto ckpt, auto large) {
+    hipLaunchKernelGGL((swiglu_kernel<decltype(pow)::value, decltype(ckpt)::value, decltype(large)::value>), grid, block,
+                       0, stream, p);
+  };
+  using std::false_type, std::true_type;
+  if (pow2) streaming ? go(true_type{}, false_type{}, true_type{}) : go(true_type{}, false_type{}, false_type{});
+  else if (p.hq) streaming ? go(false_type{}, true_type{}, true_type{}) : go(false_type{}, true_type{}, false_type{});
+  else streaming ? go(false_type{}, false_type{}, true_type{}) : go(false_type{}, false_type{}, false_type{});
   return hipGetLastError();
 }
 

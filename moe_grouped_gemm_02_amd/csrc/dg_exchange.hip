@@ -192,11 +192,13 @@ __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams
       uint4* to = reinterpret_cast<uint4*>(p.q + gr * p.cols + j * kBlockK + sub * 16);
       if constexpr (POW2) {
         uint32_t e;
-        *to = encode_bf16_tile_pow2(in[u], e);
+        const uint4 q = encode_bf16_tile_pow2(in[u], e);
+        store<U == 4>(to, q);
         if (sub == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
       } else {
         float s;
-        *to = encode_bf16_tile(in[u], s);
+        const uint4 q = encode_bf16_tile(in[u], s);
+        store<U == 4>(to, q);
         if (sub == 0) static_cast<float*>(p.sf)[sf_at] = s;
       }
     }
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
     const int r = p.rows[t * p.topk + j];
     if (r < 0 || r >= p.total_rows) continue;
     const float w = p.weights ? p.weights[t * p.topk + j] : 1.0f;
-    const uint4 v = *reinterpret_cast<const uint4*>(p.d + (int64_t)r * p.ld_d + col);
+    const uint4 v = load_streaming4(p.d + (int64_t)r * p.ld_d + col);
     const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
     if (e < entries) {
       live |= 1u << i;
       a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / (uint32_t)p.topk) * p.ld_dy + col0 + c0);
-      b[i] = *reinterpret_cast<const uint4*>(p.d + r * p.ld_d + col0 + c0);
+      b[i] = load_streaming4(p.d + r * p.ld_d + col0 + c0);
       w[i] = p.weights[e];
     }
   }

@@ -46,6 +46,35 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Stores of results larger than the L2s, which nothing reads back through them:
+// marked as streaming they leave the cached inputs alone (dispatch of 32768 x
+// 7168 rows 124 us, against 133 with plain stores; requantised transpose 84 and
+// 92, combine gradient 243 and 257).
+__device__ __forceinline__ void store_streaming(void* p, uint4 v) {
+  __builtin_nontemporal_store(v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}, static_cast<v4i*>(p));
+}
+__device__ __forceinline__ void store_streaming(void* p, uint2 v) {
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(v2i{(int)v.x, (int)v.y}, static_cast<v2i*>(p));
+}
+// Short results stay in the L2s for the kernel that takes them next.
+template <bool STREAMING>
+__device__ __forceinline__ void store(void* p, uint4 v) {
+  if constexpr (STREAMING) store_streaming(p, v);
+  else *static_cast<uint4*>(p) = v;
+}
+// Loads of values that are used once (combine of 32768 rows: 95 us, against 107
+// with plain loads).
+__device__ __forceinline__ uint4 load_streaming4(const void* p) {
+  const v4i v = __builtin_nontemporal_load(static_cast<const v4i*>(p));
+  return make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
+}
+__device__ __forceinline__ uint2 load_streaming2(const void* p) {
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  const v2i v = __builtin_nontemporal_load(static_cast<const v2i*>(p));
+  return make_uint2((uint32_t)v.x, (uint32_t)v.y);
+}
+
 // f(0) .. f(N - 1) with the index as a type, for what must be a constant.
 template <int... I, typename F>
 __device__ __forceinline__ void for_each_index(std::integer_sequence<int, I...>, F&& f) {

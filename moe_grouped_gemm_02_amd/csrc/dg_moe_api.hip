@@ -164,6 +164,7 @@ int swiglu_impl(const uint16_t* h, const int32_t* m_indices, const int32_t* mask
   DG_TRY(check_layout(rows, num_groups));
   DG_TRY(check_cols("inter", inter, 128));
   if (inter > kMaxCols / 2) return fail(DG_ERR_UNSUPPORTED_SHAPE, "inter=%d is larger than %d", inter, kMaxCols / 2);
+  if (num_groups > 65535) return fail(DG_ERR_UNSUPPORTED_SHAPE, "num_groups=%d is larger than 65535", num_groups);
   if (m_indices && masked_m) return fail(DG_ERR_INVALID_VALUE, "m_indices and masked_m given together");
   if (m_indices && num_groups != 1) return fail(DG_ERR_INVALID_VALUE, "m_indices needs num_groups == 1");
   if (!hq != !hsf) return fail(DG_ERR_INVALID_VALUE, "hq and hsf go together");

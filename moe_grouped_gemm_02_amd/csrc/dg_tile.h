@@ -217,7 +217,7 @@ __device__ __forceinline__ void tile_rows(const float (&v)[R][8], uint8_t* q, in
     const float inv = dpp<kRowLane0 + i>(t.inv);
     const uint32_t lo = e4m3_x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
     const uint32_t hi = e4m3_x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-    if ((live >> i) & 1) *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
+    if ((live >> i) & 1) store_streaming(q, make_uint2(lo, hi));
     q += ldq;
   };
   for_each_index<R>(row);
@@ -294,8 +294,8 @@ __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<
 #pragma unroll
     for (int i = 0; i < kBlockK / kColumns; ++i) {
       const int col = i * kColumns + (tid >> 3), chunk = tid & 7;
-      *reinterpret_cast<uint4*>(to[n].q + (int64_t)col * to[n].ldq + chunk * 16) =
-          *reinterpret_cast<const uint4*>(lds.codes[n] + codes_at(col, chunk));
+      store_streaming(to[n].q + (int64_t)col * to[n].ldq + chunk * 16,
+                      *reinterpret_cast<const uint4*>(lds.codes[n] + codes_at(col, chunk)));
     }
   }
 }
