@@ -34,14 +34,25 @@ __device__ __forceinline__ int local_of(int64_t i, const PlanParams& p) {
   return id >= 0 && g >= 0 && g < p.groups ? (int)g : -1;
 }
 
+// Lanes of the wave with the same local expert as this one (any, if it has none).
+__device__ __forceinline__ uint64_t same_expert(int g, int groups) {
+  uint64_t same = __ballot(g >= 0);
+  for (int bit = 1; bit < groups; bit <<= 1) {
+    const uint64_t ones = __ballot(g & bit);
+    same &= (g & bit) ? ones : ~ones;
+  }
+  return same;
+}
+
 // Counts the experts of each block's 1024 entries.
 __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) {
   __shared__ int count[kMaxLocalExperts];
   const int tid = threadIdx.x;
   const int g = local_of((int64_t)blockIdx.x * kPlanThreads + tid, p);
   if (tid < p.groups) count[tid] = 0;
+  const uint64_t same = same_expert(g, p.groups);
   __syncthreads();
-  if (g >= 0) atomicAdd(&count[g], 1);
+  if (g >= 0 && __ffsll((unsigned long long)same) - 1 == (tid & 63)) atomicAdd(&count[g], __popcll(same));
   __syncthreads();
   if (tid < p.groups) p.hist[(int64_t)blockIdx.x * p.groups + tid] = count[tid];
 }
@@ -101,12 +112,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
     const int64_t i = (int64_t)c * kPlanThreads + tid;
     if (c != first_chunk) g = local_of(i, p);
     for (int k = tid; k < kPlanWaves * p.groups; k += kPlanThreads) per_wave[k / p.groups][k % p.groups] = 0;
-    // Lanes of this wave with the same expert.
-    uint64_t same = __ballot(g >= 0);
-    for (int bit = 1; bit < p.groups; bit <<= 1) {
-      const uint64_t ones = __ballot(g & bit);
-      same &= (g & bit) ? ones : ~ones;
-    }
+    const uint64_t same = same_expert(g, p.groups);
     const int ahead = __popcll(same & ((1ull << lane) - 1ull));
     __syncthreads();
     if (g >= 0 && ahead == 0) per_wave[wave][g] = (uint16_t)__popcll(same);
@@ -181,7 +187,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams
     for (int u = 0; u < U; ++u) {
       const uint32_t e = r0 + u < total_rows ? (uint32_t)p.src[r0 + u] : ~0u;
       live[u] = e < entries;
-      if (live[u]) in[u] = load16(p.x + (int64_t)(e / (uint32_t)p.topk) * p.ld_x + j * kBlockK + sub * 16);
+      if (live[u]) in[u] = load16(p.x + (int64_t)(divided(e, p.by_topk)) * p.ld_x + j * kBlockK + sub * 16);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -258,7 +264,7 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
     w[i] = 0.0f;
     if (e < entries) {
       live |= 1u << i;
-      a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(e / (uint32_t)p.topk) * p.ld_dy + col0 + c0);
+      a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(divided(e, p.by_topk)) * p.ld_dy + col0 + c0);
       b[i] = load_streaming4(p.d + r * p.ld_d + col0 + c0);
       w[i] = p.weights[e];
     }

@@ -5,6 +5,7 @@
 #include <utility>
 
 #include "dg_device.h"
+#include "dg_moe_internal.h"
 
 namespace dg {
 
@@ -35,6 +36,11 @@ __device__ __forceinline__ Sigmoid sigmoid(float v) {
   const float e = exp_to_80(v);
   const float n = reciprocal(1.0f + e);
   return {e, n, e * n};
+}
+
+// e / d for e below 2^31 (see Divisor).
+__device__ __forceinline__ uint32_t divided(uint32_t e, Divisor d) {
+  return d.mul ? __umulhi(e, d.mul) >> d.shift : e;
 }
 
 // Between a lane's write to shared memory and another lane of the same wave

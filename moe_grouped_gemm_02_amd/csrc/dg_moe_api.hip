@@ -154,7 +154,7 @@ int dispatch_impl(const uint16_t* x, const int32_t* src, uint8_t* q, void* sf, i
   if (!x || !src || !q || !sf) return fail(DG_ERR_INVALID_VALUE, "null pointer argument");
   if (!aligned16(x) || !aligned16(q) || !aligned16(sf) || !aligned(src, 4))
     return fail(DG_ERR_MISALIGNED, "x, q and sf must be 16-byte aligned, src 4-byte aligned");
-  const dg::DispatchParams p{x, src, q, sf, tokens, topk, cols, rows, num_groups, ld_x, ld_sf};
+  const dg::DispatchParams p{x, src, q, sf, tokens, topk, cols, rows, num_groups, ld_x, ld_sf, dg::divisor(topk)};
   return launched(dg::launch_dispatch(p, pow2, static_cast<hipStream_t>(stream)), "dispatch");
 }
 
@@ -290,8 +290,8 @@ int dg_moe_combine_bwd(const uint16_t* dy, const uint16_t* d, const int32_t* src
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(DG_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
   if (!aligned16(workspace)) return fail(DG_ERR_MISALIGNED, "workspace must be 16-byte aligned");
-  const dg::CombineBwdParams p{dy,   d,    src,  rows, weights, dq,      dsf,   dqt,  dsft,   dweights, static_cast<float*>(workspace),
-                               tokens, topk, cols, m_total, ld_dy, ld_d, ld_dsf, ld_dsft};
+  const dg::CombineBwdParams p{dy,     d,    src,  rows,    weights, dq,   dsf,    dqt,     dsft, dweights, static_cast<float*>(workspace),
+                               tokens, topk, cols, m_total, ld_dy,   ld_d, ld_dsf, ld_dsft, dg::divisor(topk)};
   return launched(dg::launch_combine_bwd(p, static_cast<hipStream_t>(stream)), "combine_bwd");
 }
 

@@ -12,6 +12,21 @@ constexpr int kMaxTopk = 32;
 constexpr int kMaxExpertGroups = 64;
 constexpr int kMaxLocalExperts = 1024;
 
+// Division of numbers below 2^31 by a constant 1 <= d < 2^31: e / d is e for
+// d = 1 and otherwise (e * mul >> 32) >> shift, with mul = ceil(2^(31 + l) / d),
+// 2^l the power of two at or above d, and shift = l - 1: mul / 2^(31 + l) is above
+// 1 / d by less than 2^-(31 + l), which e < 2^31 times it cannot carry past the
+// next quotient.
+struct Divisor {
+  uint32_t mul, shift;  // mul 0: d = 1
+};
+inline Divisor divisor(uint32_t d) {
+  if (d <= 1) return {0, 0};
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l - 1};
+}
+
 struct RouteParams {
   const void* logits;  // [tokens][ld], fp32 or bf16
   const float* bias;   // null: none
@@ -53,6 +68,7 @@ struct DispatchParams {
   void* sf;
   int tokens, topk, cols, rows, groups;
   int64_t ld_x, ld_sf;
+  Divisor by_topk;
 };
 hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t stream);
 
@@ -80,6 +96,7 @@ struct CombineBwdParams {
   float* dots;  // [cols / 128][m_total] partial sums of the weights' gradient
   int tokens, topk, cols, m_total;
   int64_t ld_dy, ld_d, ld_dsf, ld_dsft;
+  Divisor by_topk;
 };
 hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream);
 

@@ -48,12 +48,19 @@ __device__ __forceinline__ void load_row(const T* row, int experts, int lane, fl
   }
 }
 
+// 1 / (1 + e^-x) within 2 ulp: the hardware's reciprocal without its Newton
+// step.
+__device__ __forceinline__ float score_sigmoid(float x) {
+  const float e = exp_to_80(x);
+  return e * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 // Scores of the wave's token.
 template <int V>
 __device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], bool sigmoid_scores) {
   if (sigmoid_scores) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]).sig;
+    for (int i = 0; i < V; ++i) s[i] = score_sigmoid(x[i]);
     return;
   }
   uint32_t most = 0;
@@ -130,9 +137,17 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
     }
     const uint32_t score = a == 0u ? 0u : p.group_top == 2 && b != 0u ? order_of(of_order(a) + of_order(b)) : a;
     int before = 0;  // groups that come first
-    for (int g = 0; g < p.groups; ++g) {
-      const uint32_t other = lane_value(score, whole ? g << p.group_shift : g);
-      before += other > score || (other == score && g < mine);
+    if (p.groups * p.groups <= 64 && whole && p.groups << p.group_shift == 64) {
+      // The lanes of a group each look at one other group.
+      const int other_group = lane & ((1 << p.group_shift) - 1);
+      const uint32_t other = (uint32_t)__shfl((int)score, other_group << p.group_shift, 64);
+      const bool first = other_group < p.groups && (other > score || (other == score && other_group < mine));
+      before = __popcll((__ballot(first) >> (mine << p.group_shift)) & ((1ull << (1 << p.group_shift)) - 1ull));
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        const uint32_t other = lane_value(score, whole ? g << p.group_shift : g);
+        before += other > score || (other == score && g < mine);
+      }
     }
     const bool stays = before < p.topk_groups && mine < p.groups && score != 0u;
     const uint64_t kept = __ballot(stays);
@@ -215,7 +230,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   float g = id >= 0 ? p.scale * p.dweights[t * p.topk + lane] : 0.0f;
   float x[V], s[V], sel = 0.0f;
   if constexpr (SIGMOID) {
-    if (id >= 0) sel = sigmoid(widen(row[id])).sig;
+    if (id >= 0) sel = score_sigmoid(widen(row[id]));
   } else {
     load_row<VEC>(row, p.experts, lane, x);
     scores<V>(x, s, false);
