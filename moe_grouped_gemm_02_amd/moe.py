@@ -93,8 +93,9 @@ def _rows_of(t, name, dtypes, ndim=2):
     """A matrix with unit stride in its rows; returns its row stride."""
     if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes:
         stride = t.stride()
-        if len(stride) == ndim and stride[-1] == 1 and t.shape[-2] > 1 and t.numel():
-            return stride[-2]
+        if len(stride) == ndim and stride[-1] == 1 and t.numel():
+            # (the stride of a single row says nothing)
+            return stride[-2] if t.shape[-2] > 1 else (t.shape[-1] + 7) // 8 * 8
     _expect(t, name, dtypes, ndim)
     if t.shape[-2] <= 1 or t.numel() == 0:  # such strides say nothing
         if t.shape[-1] > 1 and t.numel():
