@@ -249,9 +249,10 @@ int dg_grouped_masked_ue8m0_qout(const uint8_t* a, const uint8_t* sfa, const uin
  *       one scale per row of B and 128-wide K slice (dg_quant_1x128 of B)
  *   d   [num_groups][m][n] bf16
  *   k_offsets [num_groups + 1] int32 (device): 0 = k_offsets[0] <= ... <=
- *       k_offsets[num_groups] = k, multiples of 128 (precondition; values are
+ *       k_offsets[num_groups] <= k, multiples of 128 (precondition; values are
  *       clamped to [0, k] and rounded down to a slice, so nothing is read out
- *       of bounds for any content).  An empty group writes zeros.
+ *       of bounds for any content).  An empty group writes zeros; slices past
+ *       k_offsets[num_groups] belong to no group and are not read.
  * Rules as for dg_fp8_gemm_nt with lda = ldb = k and ldd = n, plus n % 8 == 0.
  * Needs no workspace (pass NULL, 0).  Data-parallel over (group, M tile,
  * N tile) units.

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) 
   if (j >= tiles) return;
   const int64_t g = blockIdx.z;
   const int rows = p.masked_m ? min(p.masked_m[g], p.rows) : p.rows;
-  for (int r = blockIdx.y * kRowWaves + (threadIdx.x >> 6); r < rows; r += gridDim.y * kRowWaves) {
+  for (int64_t r = blockIdx.y * kRowWaves + (threadIdx.x >> 6); r < rows; r += gridDim.y * kRowWaves) {
     if (p.m_indices && p.m_indices[r] < 0) continue;
     const int64_t gr = g * p.rows + r;
     const int col = j * kBlockK + sub * 16;

@@ -59,7 +59,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) 
 
 // Places the entries and fills the index arrays of the layout's rows.  ONE: one
 // workgroup, which counts the entries itself; otherwise block b places entries
-// [1024 b, 1024 b + 1024) with the counts of all blocks.
+// [1024 b, 1024 b + 1024) with the counts of all blocks (blocks past the last
+// entry help with the rows alone).
 template <bool ONE>
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) {
   __shared__ int start[kMaxLocalExperts + 1];  // first row of each group
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
       if (e >= 0) atomicAdd(&count[e], 1);
     }
   } else {
-    const int before = blockIdx.x * p.groups, all = gridDim.x * p.groups;
+    const int before = blockIdx.x * p.groups, all = p.blocks * p.groups;
     for (int i = tid; i < all; i += kPlanThreads) {
       const int v = p.hist[i], e = i % p.groups;
       atomicAdd(&count[e], v);
@@ -325,13 +326,17 @@ size_t plan_workspace_bytes(int64_t entries, int groups) {
   return (size_t)plan_blocks(entries) * groups * sizeof(int32_t);
 }
 
-hipError_t launch_plan(const PlanParams& p, hipStream_t stream) {
-  const dim3 grid(plan_blocks(p.entries)), block(kPlanThreads);
+hipError_t launch_plan(const PlanParams& params, hipStream_t stream) {
+  PlanParams p = params;
+  p.blocks = plan_blocks(p.entries);
+  const dim3 block(kPlanThreads);
   if (p.entries <= kOnePlanEntries && p.layout_rows <= kOnePlanRows) {
     hipLaunchKernelGGL(plan_place_kernel<true>, dim3(1), block, 0, stream, p);
   } else {
-    hipLaunchKernelGGL(plan_count_kernel, grid, block, 0, stream, p);
-    hipLaunchKernelGGL(plan_place_kernel<false>, grid, block, 0, stream, p);
+    const int for_rows = (int)(((int64_t)p.layout_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
+    const int most = for_rows < 256 ? for_rows : 256;
+    hipLaunchKernelGGL(plan_count_kernel, dim3(p.blocks), block, 0, stream, p);
+    hipLaunchKernelGGL(plan_place_kernel<false>, dim3(p.blocks > most ? p.blocks : most), block, 0, stream, p);
   }
   return hipGetLastError();
 }

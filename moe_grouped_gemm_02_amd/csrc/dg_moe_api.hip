@@ -58,6 +58,13 @@ int check_layout(int rows, int groups) {
   return DG_SUCCESS;
 }
 
+// Tiles of 128 x 128 that a grid counts with 32 bits.
+int check_tiles(int rows, int cols) {
+  if ((int64_t)(rows / 128) * (cols / 128) >= kRowLimit)
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "2^31 or more tiles (%d x %d)", rows, cols);
+  return DG_SUCCESS;
+}
+
 #define DG_TRY(call)                      \
   do {                                    \
     const int st_ = (call);               \
@@ -275,6 +282,7 @@ int dg_moe_combine_bwd(const uint16_t* dy, const uint16_t* d, const int32_t* src
   DG_TRY(check_layout(m_total, 1));
   if (m_total % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m_total=%d is not a multiple of 128", m_total);
   DG_TRY(check_cols("cols", cols, 128));
+  DG_TRY(check_tiles(m_total, cols));
   if (!dqt != !dsft) return fail(DG_ERR_INVALID_VALUE, "dqt and dsft go together");
   DG_TRY(check_ld("ld_dy", ld_dy, cols, 8, tokens, 2));
   DG_TRY(check_ld("ld_d", ld_d, cols, 8, m_total, 2));
@@ -316,6 +324,7 @@ int dg_swiglu_bwd(const uint8_t* hq, const float* hsf, const uint16_t* dact, con
   if (m_total % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m_total=%d is not a multiple of 128", m_total);
   DG_TRY(check_cols("inter", inter, 128));
   if (inter > kMaxCols / 2) return fail(DG_ERR_UNSUPPORTED_SHAPE, "inter=%d is larger than %d", inter, kMaxCols / 2);
+  DG_TRY(check_tiles(m_total, inter));
   if (!aqt != !asft) return fail(DG_ERR_INVALID_VALUE, "aqt and asft go together");
   DG_TRY(check_ld("ld_hsf", ld_hsf, m_total, 4, inter / 64, 4));
   DG_TRY(check_ld("ld_dact", ld_dact, inter, 8, m_total, 2));
@@ -337,6 +346,7 @@ int dg_requant_t(const uint8_t* q, const float* sf, const int32_t* m_indices, ui
   DG_TRY(check_layout(rows, 1));
   if (rows % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "rows=%d is not a multiple of 128", rows);
   DG_TRY(check_cols("cols", cols, 128));
+  DG_TRY(check_tiles(rows, cols));
   DG_TRY(check_ld("ld_sf", ld_sf, rows, 4, cols / 128, 4));
   DG_TRY(check_ld("ld_sft", ld_sft, cols, 4, rows / 128, 4));
   if (rows == 0 || cols == 0) return ok();

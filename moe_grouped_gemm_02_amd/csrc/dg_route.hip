@@ -5,8 +5,10 @@
 // of two that covers all experts, so that a row is one vector load a lane, the
 // order of lanes and registers is the order of the experts (ties), and every
 // reduction stays in registers (row operations and readlane, no shared memory).
-// A token is read once; what bounds the kernels is the issue of vector
-// instructions, about 250 a token of 256 experts.
+// A token is read once.  What bounds the choice is the issue of vector
+// instructions, about 410 a token of 256 experts in groups (19 a round of the
+// top-k, 11 a sigmoid): 32768 tokens in 21.5 us, 59 us with shuffles for the row
+// operations and 64-bit keys.  The gradient is bound by what it writes: 10.9 us.
 
 #include "dg_math.h"
 #include "dg_moe_internal.h"
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
   if constexpr (GROUPS) {
     // Two largest keys of each group: in groups of 2^n whole lanes by row
     // operations, otherwise lane g walks group g in shared memory (256 experts in
-    // 8 groups, 32768 tokens: the walk costs 22 us more).
+    // 8 groups, 32768 tokens: 21.5 us, and 32.6 by the walk).
     uint32_t a = 0, b = 0;
     const bool whole = p.group_shift >= 0;
     const int mine = whole ? lane >> p.group_shift : lane;  // the group this lane holds the score of
@@ -138,7 +140,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
     const uint32_t score = a == 0u ? 0u : p.group_top == 2 && b != 0u ? order_of(of_order(a) + of_order(b)) : a;
     int before = 0;  // groups that come first
     if (p.groups * p.groups <= 64 && whole && p.groups << p.group_shift == 64) {
-      // The lanes of a group each look at one other group.
+      // The lanes of a group each look at one other group (23.1 us with the loop
+      // below).
       const int other_group = lane & ((1 << p.group_shift) - 1);
       const uint32_t other = (uint32_t)__shfl((int)score, other_group << p.group_shift, 64);
       const bool first = other_group < p.groups && (other > score || (other == score && other_group < mine));
@@ -276,7 +279,8 @@ void go(const RouteParams& p, bool bwd, hipStream_t stream) {
   else hipLaunchKernelGGL((route_bwd_kernel<VEC, T, V, false>), grid, block, 0, stream, p);
 }
 
-// Whole vectors: no ragged last lane, and every row starts on a vector.
+// Whole vectors: no ragged last lane, and every row starts on a vector (21.5 us
+// against 23.5 with single elements).
 template <typename T, int V>
 void go(RouteParams p, bool bwd, hipStream_t stream) {
   p.group_shift = -1;

@@ -50,7 +50,7 @@ PLANS = [  # tokens, topk, experts, first, groups, contiguous rows, masked rows
     (0, 2, 4, 0, 4, 256, 8), (1, 1, 1, 0, 1, 128, 1), (1, 8, 256, 0, 256, 1024, 4), (7, 3, 9, 4, 3, 512, 5),
     (128, 8, 256, 64, 32, 4096, 128), (1000, 4, 16, 0, 16, 6144, 300), (1000, 4, 16, 12, 4, 640, 100),
     (5000, 8, 40, 8, 8, 9216, 1024), (9001, 2, 1024, 0, 1024, 131072, 16), (300, 32, 33, 1, 32, 0, 0),
-    (20011, 6, 6, 2, 1, 20096, 20011)]
+    (20011, 6, 6, 2, 1, 20096, 20011), (100, 4, 64, 0, 64, 262144, 8192)]
 
 
 @pytest.mark.parametrize("case", PLANS, ids=str)

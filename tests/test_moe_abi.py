@@ -101,6 +101,8 @@ BAD = [
     ("dg_swiglu_bwd", dict(m_total=64), SHAPE), ("dg_swiglu_bwd", dict(ld_dact=508), INVALID),
     ("dg_swiglu_bwd", dict(ld_dsft=1020), INVALID), ("dg_swiglu_bwd", dict(aqt=0), INVALID),
     ("dg_swiglu_bwd", dict(dqt=0), INVALID), ("dg_swiglu_bwd", dict(inter=1 << 22, ld_dact=1 << 22, ld_dsft=1 << 23), SHAPE),
+    ("dg_requant_t", dict(rows=2**31 - 128, cols=65535 * 128, ld_sf=2**31 - 128, ld_sft=65535 * 128), SHAPE),
+    ("dg_swiglu_quant", dict(num_groups=65536, rows=4, ld_sf=4, ld_hsf=4), SHAPE),
     ("dg_requant_t", dict(rows=100), SHAPE), ("dg_requant_t", dict(cols=130), SHAPE),
     ("dg_requant_t", dict(ld_sft=508), INVALID), ("dg_requant_t", dict(ld_sf=258), MISALIGNED),
     ("dg_requant_t", dict(qt=0), INVALID), ("dg_requant_t", dict(sf=FAKE + 4), MISALIGNED),
