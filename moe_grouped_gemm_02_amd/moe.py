@@ -52,9 +52,10 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def _score(score):
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
-    return _SCORES[score]
+    try:
+        return _SCORES[score]
+    except (KeyError, TypeError):
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}") from None
 
 
 # Stream handle of a device's current stream: what torch.cuda.current_stream()
@@ -71,71 +72,107 @@ def _shape(t, name, want):
         raise ValueError(f"{name} must have shape {tuple(want)}, has {tuple(t.shape)}")
 
 
+# The checks ask a tensor for as little as they can, since each question costs a
+# small call about 0.1 us: what is in order passes on one line, anything else
+# goes through the questions one by one for its error.
+
 def _dense(t, name, dtypes, want):
-    """A contiguous tensor of the given shape."""
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == want and t.is_contiguous():
-        return
+    """Address of a contiguous tensor of the given shape."""
+    try:
+        if t.is_cuda and t.dtype in dtypes and t.shape == want and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _expect(t, name, dtypes, len(want))
     _shape(t, name, want)
     _contig(t, name)
+    return t.data_ptr()
+
+
+def _dense_or_none(t, name, dtypes, want):
+    return None if t is None else _dense(t, name, dtypes, want)
 
 
 def _topk(t, name, tokens):
-    """Slots of an index matrix [tokens][topk]."""
-    if type(t) is not torch.Tensor or t.dim() != 2:
+    """Address and slots of an index matrix [tokens][topk]."""
+    try:
+        topk = t.shape[1]
+    except (AttributeError, IndexError):
         _expect(t, name, _I32, 2)
-    topk = t.shape[1]
-    _dense(t, name, _I32, (tokens, topk))
-    return topk
+        raise
+    return _dense(t, name, _I32, (tokens, topk)), topk
 
 
-def _rows_of(t, name, dtypes, ndim=2):
-    """A matrix with unit stride in its rows; returns its row stride."""
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes:
-        stride = t.stride()
-        if len(stride) == ndim and stride[-1] == 1 and t.numel():
-            # (the stride of a single row says nothing)
-            return stride[-2] if t.shape[-2] > 1 else (t.shape[-1] + 7) // 8 * 8
-    _expect(t, name, dtypes, ndim)
-    if t.shape[-2] <= 1 or t.numel() == 0:  # such strides say nothing
-        if t.shape[-1] > 1 and t.numel():
+def _matrix(t, name, dtypes):
+    """Address, rows, columns and row stride of a matrix with unit stride in its
+    rows.  (The stride of a single row says nothing.)"""
+    try:
+        if t.is_cuda and t.dtype in dtypes:
+            rows, cols = t.shape
+            ld, unit = t.stride()
+            if unit == 1 and rows and cols:
+                return t.data_ptr(), rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
+    except (AttributeError, ValueError):
+        pass
+    _expect(t, name, dtypes, 2)
+    rows, cols = t.shape
+    if rows <= 1 or cols == 0:
+        if cols > 1 and rows:
             _row_major(t, name)
-        return (t.shape[-1] + 7) // 8 * 8
+        return t.data_ptr(), rows, cols, (cols + 7) // 8 * 8
     _row_major(t, name)
-    return t.stride(-2)
+    return t.data_ptr(), rows, cols, t.stride(0)
+
+
+def _dense_groups(t, name, dtypes, want):
+    """Address and row stride of matrices [G][rows][cols] one after another, with
+    unit stride in their rows."""
+    groups, rows, cols = want
+    try:
+        if t.is_cuda and t.dtype in dtypes and t.shape == want and rows > 1 and cols:
+            step, ld, unit = t.stride()
+            if unit == 1 and (groups == 1 or step == rows * ld):
+                return t.data_ptr(), ld
+    except AttributeError:
+        pass
+    _expect(t, name, dtypes, 3)
+    _shape(t, name, want)
+    if cols > 1 and t.numel():
+        _row_major(t, name)
+    ld = t.stride(1) if rows > 1 and t.numel() else (cols + 7) // 8 * 8
+    if groups > 1 and t.numel() and t.stride(0) != rows * ld:
+        raise ValueError(f"{name} must have its groups one after another")
+    return t.data_ptr(), ld
 
 
 def _scales(t, name, dtypes, lead, rows):
-    """A contiguous scale matrix [*lead][ld] with ld >= rows; returns ld."""
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
-        shape = t.shape
-        if shape[:-1] == lead and shape[-1] >= rows:
-            return shape[-1]
+    """Address and ld of a contiguous scale matrix [*lead][ld] with ld >= rows."""
+    try:
+        if t.is_cuda and t.dtype in dtypes and t.is_contiguous():
+            shape = t.shape
+            ld = shape[-1]
+            if ld >= rows and shape == (*lead, ld):
+                return t.data_ptr(), ld
+    except (AttributeError, IndexError):
+        pass
     _expect(t, name, dtypes, len(lead) + 1)
     _shape(t, name, (*lead, t.shape[-1]))
     if t.shape[-1] < rows:
         raise ValueError(f"{name} has {t.shape[-1]} columns, needs {rows}")
     _contig(t, name)
-    return t.shape[-1]
-
-
-def _call(name, *args):
-    status = _FUNCTIONS[name](*args)
-    if status != 0:
-        _check(name, status)
+    return t.data_ptr(), t.shape[-1]
 
 
 # ---------------------------------------------------------------- routing --
 
 def _route(fn, dtypes, logits, ids, weights, bias, score, expert_groups, topk_groups, group_top, renormalize, scale):
-    ld = _rows_of(logits, "logits", dtypes)
-    tokens, experts = logits.shape
-    topk = _topk(ids, "ids", tokens)
-    _dense(weights, "weights", _F32, (tokens, topk))
-    if bias is not None:
-        _dense(bias, "bias", _F32, (experts,))
-    _call(fn, _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), tokens, experts, topk, ld, _score(score),
-          int(expert_groups), int(topk_groups), int(group_top), int(bool(renormalize)), float(scale), _stream(logits))
+    logits_at, tokens, experts, ld = _matrix(logits, "logits", dtypes)
+    ids_at, topk = _topk(ids, "ids", tokens)
+    weights_at = _dense(weights, "weights", _F32, (tokens, topk))
+    bias_at = _dense_or_none(bias, "bias", _F32, (experts,))
+    _check(fn, _FUNCTIONS[fn](
+        logits_at, bias_at, ids_at, weights_at, tokens, experts, topk, ld, _score(score), int(expert_groups),
+        int(topk_groups), int(group_top), bool(renormalize), scale, _stream(logits)))
     return ids, weights
 
 
@@ -161,14 +198,15 @@ def dg_moe_route_bf16(logits, ids, weights, bias=None, score="softmax", expert_g
 
 
 def _route_bwd(fn, dtypes, logits, ids, dweights, dlogits, score, renormalize, scale):
-    ld = _rows_of(logits, "logits", dtypes)
-    tokens, experts = logits.shape
-    topk = _topk(ids, "ids", tokens)
-    _dense(dweights, "dweights", _F32, (tokens, topk))
-    ld_d = _rows_of(dlogits, "dlogits", dtypes)
-    _shape(dlogits, "dlogits", (tokens, experts))
-    _call(fn, _ptr(logits), _ptr(ids), _ptr(dweights), _ptr(dlogits), tokens, experts, topk, ld, ld_d, _score(score),
-          int(bool(renormalize)), float(scale), _stream(logits))
+    logits_at, tokens, experts, ld = _matrix(logits, "logits", dtypes)
+    ids_at, topk = _topk(ids, "ids", tokens)
+    dweights_at = _dense(dweights, "dweights", _F32, (tokens, topk))
+    dlogits_at, rows_d, cols_d, ld_d = _matrix(dlogits, "dlogits", dtypes)
+    if rows_d != tokens or cols_d != experts:
+        _shape(dlogits, "dlogits", (tokens, experts))
+    _check(fn, _FUNCTIONS[fn](
+        logits_at, ids_at, dweights_at, dlogits_at, tokens, experts, topk, ld, ld_d, _score(score), bool(renormalize),
+        scale, _stream(logits)))
     return dlogits
 
 
@@ -186,20 +224,27 @@ def dg_moe_route_bwd_bf16(logits, ids, dweights, dlogits, score="softmax", renor
 # --------------------------------------------------------------- exchange --
 
 def _vector(t, name):
-    """Length of a contiguous vector of indices."""
-    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous()):
-        _expect(t, name, _I32, 1)
-        _contig(t, name)
-    return t.shape[0]
+    """Address and length of a contiguous vector of indices."""
+    try:
+        if t.is_cuda and t.dtype is torch.int32 and t.is_contiguous():
+            n, = t.shape
+            return t.data_ptr(), n
+    except (AttributeError, ValueError):
+        pass
+    _expect(t, name, _I32, 1)
+    _contig(t, name)
+    return t.data_ptr(), t.shape[0]
 
 
 def _entries(ids, rows):
-    if type(ids) is not torch.Tensor or ids.dim() != 2:
+    """Addresses and shape of the routed ids and their rows."""
+    try:
+        tokens, topk = ids.shape
+    except (AttributeError, ValueError):
         _expect(ids, "ids", _I32, 2)
-    shape = ids.shape
-    _dense(ids, "ids", _I32, shape)
-    _dense(rows, "rows", _I32, shape)
-    return shape
+        raise
+    shape = tokens, topk
+    return _dense(ids, "ids", _I32, shape), _dense(rows, "rows", _I32, shape), tokens, topk
 
 
 def dg_get_moe_plan_workspace_size(tokens, topk, num_groups):
@@ -210,48 +255,59 @@ def dg_moe_plan_contiguous(ids, rows, src, m_indices, k_offsets, first_expert=0,
     """Row plan of the contiguous layout: ids [T][k] -> rows [T][k], and per
     layout row src (entry t * k + j or -1) and m_indices (group or -1), and
     k_offsets [G+1], all int32.  Group g is expert first_expert + g."""
-    tokens, topk = _entries(ids, rows)
-    m_total = _vector(src, "src")
-    _dense(m_indices, "m_indices", _I32, (m_total,))
-    groups = _vector(k_offsets, "k_offsets") - 1
-    _call("dg_moe_plan_contiguous", _ptr(ids), _ptr(rows), _ptr(src), _ptr(m_indices), _ptr(k_offsets), tokens, topk,
-          int(first_expert), groups, m_total, _ptr(workspace), _ws(workspace), _stream(ids))
+    ids_at, rows_at, tokens, topk = _entries(ids, rows)
+    src_at, m_total = _vector(src, "src")
+    m_indices_at = _dense(m_indices, "m_indices", _I32, (m_total,))
+    k_offsets_at, ends = _vector(k_offsets, "k_offsets")
+    _check("dg_moe_plan_contiguous", _lib.dg_moe_plan_contiguous(
+        ids_at, rows_at, src_at, m_indices_at, k_offsets_at, tokens, topk, int(first_expert), ends - 1, m_total,
+        _ptr(workspace), _ws(workspace), _stream(ids)))
     return rows, src, m_indices, k_offsets
 
 
 def dg_moe_plan_masked(ids, rows, src, masked_m, first_expert=0, workspace=None):
     """Row plan of the masked layout: src holds G * M_max entries, masked_m [G]."""
-    tokens, topk = _entries(ids, rows)
-    groups, layout_rows = _vector(masked_m, "masked_m"), _vector(src, "src")
+    ids_at, rows_at, tokens, topk = _entries(ids, rows)
+    masked_m_at, groups = _vector(masked_m, "masked_m")
+    src_at, layout_rows = _vector(src, "src")
     if groups < 1 or layout_rows % groups:
         raise ValueError("src must hold the same number of rows for every group")
-    _call("dg_moe_plan_masked", _ptr(ids), _ptr(rows), _ptr(src), _ptr(masked_m), tokens, topk, int(first_expert),
-          groups, layout_rows // groups, _ptr(workspace), _ws(workspace), _stream(ids))
+    _check("dg_moe_plan_masked", _lib.dg_moe_plan_masked(
+        ids_at, rows_at, src_at, masked_m_at, tokens, topk, int(first_expert), groups, layout_rows // groups,
+        _ptr(workspace), _ws(workspace), _stream(ids)))
     return rows, src, masked_m
 
 
 def _codes(q, sf, sf_dtypes):
-    """(groups, rows, cols, ld) of codes [(G)][rows][cols] and scales [(G)][cols/128][ld]."""
-    if not (type(q) is torch.Tensor and q.is_cuda and q.dtype in _U8 and q.is_contiguous()):
+    """Addresses, (groups, rows, cols) and ld of codes [(G)][rows][cols] and
+    scales [(G)][cols/128][ld]."""
+    try:
+        fine = q.is_cuda and q.dtype in _U8 and q.is_contiguous()
+    except AttributeError:
+        fine = False
+    if not fine:
         _expect(q, "q", _U8)
         _contig(q, "q")
     shape = q.shape
     if len(shape) == 2:
-        rows, cols = shape
-        return 1, rows, cols, _scales(sf, "sf", sf_dtypes, (cols // 128,), rows)
-    if len(shape) == 3:
+        groups, (rows, cols) = 1, shape
+        sf_at, ld = _scales(sf, "sf", sf_dtypes, (cols // 128,), rows)
+    elif len(shape) == 3:
         groups, rows, cols = shape
-        return groups, rows, cols, _scales(sf, "sf", sf_dtypes, (groups, cols // 128), rows)
-    raise ValueError("q must have 2 or 3 dimensions")
+        sf_at, ld = _scales(sf, "sf", sf_dtypes, (groups, cols // 128), rows)
+    else:
+        raise ValueError("q must have 2 or 3 dimensions")
+    return q.data_ptr(), sf_at, groups, rows, cols, ld
 
 
 def _dispatch(fn, sf_dtypes, x, src, q, sf, topk):
-    ld_x = _rows_of(x, "x", _BF)
-    groups, rows, cols, ld_sf = _codes(q, sf, sf_dtypes)
-    if x.shape[1] != cols:
+    x_at, tokens, x_cols, ld_x = _matrix(x, "x", _BF)
+    q_at, sf_at, groups, rows, cols, ld_sf = _codes(q, sf, sf_dtypes)
+    if x_cols != cols:
         raise ValueError("x and q must have the same number of columns")
-    _dense(src, "src", _I32, (groups * rows,))
-    _call(fn, _ptr(x), _ptr(src), _ptr(q), _ptr(sf), x.shape[0], int(topk), cols, rows, groups, ld_x, ld_sf, _stream(x))
+    src_at = _dense(src, "src", _I32, (groups * rows,))
+    _check(fn, _FUNCTIONS[fn](
+        x_at, src_at, q_at, sf_at, tokens, int(topk), cols, rows, groups, ld_x, ld_sf, _stream(x)))
     return q, sf
 
 
@@ -270,19 +326,17 @@ def dg_moe_dispatch_ue8m0(x, src, q, sf, topk):
 def dg_moe_combine(d, rows, y, weights=None):
     """y[t] = sum_j weights[t][j] * d[rows[t][j]] (weights None: ones); d [M][C]
     or [G][M_max][C] bf16, y [T][C] bf16.  Rows outside d add nothing."""
-    _expect(d, "d", _BF)
-    if d.dim() == 3:
+    if isinstance(d, torch.Tensor) and d.dim() == 3:
         _contig(d, "d")
         d = d.view(-1, d.shape[-1])
-    ld_d, ld_y = _rows_of(d, "d", _BF), _rows_of(y, "y", _BF)
-    tokens, cols = y.shape
-    if d.shape[1] != cols:
+    d_at, total_rows, d_cols, ld_d = _matrix(d, "d", _BF)
+    y_at, tokens, cols, ld_y = _matrix(y, "y", _BF)
+    if d_cols != cols:
         raise ValueError("d and y must have the same number of columns")
-    topk = _topk(rows, "rows", tokens)
-    if weights is not None:
-        _dense(weights, "weights", _F32, (tokens, topk))
-    _call("dg_moe_combine", _ptr(d), _ptr(rows), _ptr(weights), _ptr(y), tokens, topk, cols, d.shape[0], ld_d, ld_y,
-          _stream(y))
+    rows_at, topk = _topk(rows, "rows", tokens)
+    weights_at = _dense_or_none(weights, "weights", _F32, (tokens, topk))
+    _check("dg_moe_combine", _lib.dg_moe_combine(
+        d_at, rows_at, weights_at, y_at, tokens, topk, cols, total_rows, ld_d, ld_y, _stream(y)))
     return y
 
 
@@ -294,39 +348,40 @@ def dg_moe_combine_bwd(dy, d, src, rows, weights, dq, dsf, dqt, dsft, dweights, 
     """Gradient of dg_moe_combine over a contiguous layout: the expert rows'
     gradient as codes dq [M][C] / dsf [C/128][ld] and transposed dqt [C][M] /
     dsft [M/128][ld] (both None: left out), and dweights [T][k]."""
-    ld_dy, ld_d = _rows_of(dy, "dy", _BF), _rows_of(d, "d", _BF)
-    tokens, cols = dy.shape
-    m_total = d.shape[0]
-    _shape(d, "d", (m_total, cols))
-    _dense(src, "src", _I32, (m_total,))
-    topk = _topk(rows, "rows", tokens)
-    _dense(weights, "weights", _F32, (tokens, topk))
-    _dense(dweights, "dweights", _F32, (tokens, topk))
-    _dense(dq, "dq", _U8, (m_total, cols))
-    ld_dsf, ld_dsft = _scales(dsf, "dsf", _F32, (cols // 128,), m_total), 0
+    dy_at, tokens, cols, ld_dy = _matrix(dy, "dy", _BF)
+    d_at, m_total, d_cols, ld_d = _matrix(d, "d", _BF)
+    if d_cols != cols:
+        _shape(d, "d", (m_total, cols))
+    src_at = _dense(src, "src", _I32, (m_total,))
+    rows_at, topk = _topk(rows, "rows", tokens)
+    entries = tokens, topk
+    weights_at = _dense(weights, "weights", _F32, entries)
+    dweights_at = _dense(dweights, "dweights", _F32, entries)
+    dq_at = _dense(dq, "dq", _U8, (m_total, cols))
+    dsf_at, ld_dsf = _scales(dsf, "dsf", _F32, (cols // 128,), m_total)
+    dqt_at, dsft_at, ld_dsft = None, None, 0
     if dqt is not None or dsft is not None:
-        _dense(dqt, "dqt", _U8, (cols, m_total))
-        ld_dsft = _scales(dsft, "dsft", _F32, (m_total // 128,), cols)
-    _call("dg_moe_combine_bwd", _ptr(dy), _ptr(d), _ptr(src), _ptr(rows), _ptr(weights), _ptr(dq), _ptr(dsf), _ptr(dqt),
-          _ptr(dsft), _ptr(dweights), tokens, topk, cols, m_total, ld_dy, ld_d, ld_dsf, ld_dsft, _ptr(workspace),
-          _ws(workspace), _stream(dy))
+        dqt_at = _dense(dqt, "dqt", _U8, (cols, m_total))
+        dsft_at, ld_dsft = _scales(dsft, "dsft", _F32, (m_total // 128,), cols)
+    _check("dg_moe_combine_bwd", _lib.dg_moe_combine_bwd(
+        dy_at, d_at, src_at, rows_at, weights_at, dq_at, dsf_at, dqt_at, dsft_at, dweights_at, tokens, topk, cols,
+        m_total, ld_dy, ld_d, ld_dsf, ld_dsft, _ptr(workspace), _ws(workspace), _stream(dy)))
     return dq, dsf, dqt, dsft, dweights
 
 
 # ------------------------------------------------------------ checkpoints --
 
 def _swiglu_args(h, q, sf, sf_dtypes, m_indices, masked_m):
-    groups, rows, inter, ld_sf = _codes(q, sf, sf_dtypes)
-    ld_h = _rows_of(h, "h", _BF, q.dim())
-    if h.shape != ((rows, 2 * inter) if q.dim() == 2 else (groups, rows, 2 * inter)):
-        _shape(h, "h", (*q.shape[:-1], 2 * inter))
-    if groups > 1 and h.stride(0) != rows * ld_h:
-        raise ValueError("h must have its groups one after another")
-    if m_indices is not None:
-        _dense(m_indices, "m_indices", _I32, (rows,))
-    if masked_m is not None:
-        _dense(masked_m, "masked_m", _I32, (groups,))
-    return groups, rows, inter, ld_h, ld_sf
+    q_at, sf_at, groups, rows, inter, ld_sf = _codes(q, sf, sf_dtypes)
+    if q.dim() == 2:
+        h_at, h_rows, h_cols, ld_h = _matrix(h, "h", _BF)
+        if h_rows != rows or h_cols != 2 * inter:
+            _shape(h, "h", (rows, 2 * inter))
+    else:
+        h_at, ld_h = _dense_groups(h, "h", _BF, (groups, rows, 2 * inter))
+    m_indices_at = _dense_or_none(m_indices, "m_indices", _I32, (rows,))
+    masked_m_at = _dense_or_none(masked_m, "masked_m", _I32, (groups,))
+    return h_at, m_indices_at, masked_m_at, q_at, sf_at, groups, rows, inter, ld_h, ld_sf
 
 
 def dg_swiglu_quant(h, q, sf, m_indices=None, masked_m=None, hq=None, hsf=None):
@@ -334,21 +389,24 @@ def dg_swiglu_quant(h, q, sf, m_indices=None, masked_m=None, hq=None, hsf=None):
     [G][M_max][2I]; with hq and hsf also the codes of h, its 8-bit checkpoint.
     Rows with m_indices < 0 (contiguous) or past masked_m[g] (masked) are not
     written."""
-    groups, rows, inter, ld_h, ld_sf = _swiglu_args(h, q, sf, _F32, m_indices, masked_m)
-    ld_hsf = 0
+    h_at, m_indices_at, masked_m_at, q_at, sf_at, groups, rows, inter, ld_h, ld_sf = _swiglu_args(
+        h, q, sf, _F32, m_indices, masked_m)
+    hq_at, hsf_at, ld_hsf = None, None, 0
     if hq is not None or hsf is not None:
-        _dense(hq, "hq", _U8, h.shape)
-        ld_hsf = _scales(hsf, "hsf", _F32, (*q.shape[:-2], 2 * inter // 128), rows)
-    _call("dg_swiglu_quant", _ptr(h), _ptr(m_indices), _ptr(masked_m), _ptr(q), _ptr(sf), _ptr(hq), _ptr(hsf), rows, inter,
-          groups, ld_h, ld_sf, ld_hsf, _stream(h))
+        hq_at = _dense(hq, "hq", _U8, h.shape)
+        hsf_at, ld_hsf = _scales(hsf, "hsf", _F32, (*q.shape[:-2], 2 * inter // 128), rows)
+    _check("dg_swiglu_quant", _lib.dg_swiglu_quant(
+        h_at, m_indices_at, masked_m_at, q_at, sf_at, hq_at, hsf_at, rows, inter, groups, ld_h, ld_sf, ld_hsf,
+        _stream(h)))
     return q, sf
 
 
 def dg_swiglu_quant_ue8m0(h, q, sf, m_indices=None, masked_m=None):
     """dg_swiglu_quant with exponent-byte scales, without a checkpoint."""
-    groups, rows, inter, ld_h, ld_sf = _swiglu_args(h, q, sf, _E8, m_indices, masked_m)
-    _call("dg_swiglu_quant_ue8m0", _ptr(h), _ptr(m_indices), _ptr(masked_m), _ptr(q), _ptr(sf), rows, inter, groups, ld_h,
-          ld_sf, _stream(h))
+    h_at, m_indices_at, masked_m_at, q_at, sf_at, groups, rows, inter, ld_h, ld_sf = _swiglu_args(
+        h, q, sf, _E8, m_indices, masked_m)
+    _check("dg_swiglu_quant_ue8m0", _lib.dg_swiglu_quant_ue8m0(
+        h_at, m_indices_at, masked_m_at, q_at, sf_at, rows, inter, groups, ld_h, ld_sf, _stream(h)))
     return q, sf
 
 
@@ -357,21 +415,22 @@ def dg_swiglu_bwd(hq, hsf, dact, m_indices, dq, dsf, dqt, dsft, aqt=None, asft=N
     gradient dact [M][I] bf16 of its output: codes of dh by rows (dq, dsf) and
     transposed (dqt [2I][M], dsft [M/128][ld]), and with aqt and asft the
     transposed codes [I][M] of the unit's output."""
-    ld_dact = _rows_of(dact, "dact", _BF)
-    m_total, inter = dact.shape
-    _dense(hq, "hq", _U8, (m_total, 2 * inter))
-    _dense(dq, "dq", _U8, (m_total, 2 * inter))
-    _dense(dqt, "dqt", _U8, (2 * inter, m_total))
-    if m_indices is not None:
-        _dense(m_indices, "m_indices", _I32, (m_total,))
-    ld_hsf = _scales(hsf, "hsf", _F32, (2 * inter // 128,), m_total)
-    ld_dsf = _scales(dsf, "dsf", _F32, (2 * inter // 128,), m_total)
-    ld_dsft, ld_asft = _scales(dsft, "dsft", _F32, (m_total // 128,), 2 * inter), 0
+    dact_at, m_total, inter, ld_dact = _matrix(dact, "dact", _BF)
+    both = 2 * inter
+    hq_at = _dense(hq, "hq", _U8, (m_total, both))
+    dq_at = _dense(dq, "dq", _U8, (m_total, both))
+    dqt_at = _dense(dqt, "dqt", _U8, (both, m_total))
+    m_indices_at = _dense_or_none(m_indices, "m_indices", _I32, (m_total,))
+    hsf_at, ld_hsf = _scales(hsf, "hsf", _F32, (both // 128,), m_total)
+    dsf_at, ld_dsf = _scales(dsf, "dsf", _F32, (both // 128,), m_total)
+    dsft_at, ld_dsft = _scales(dsft, "dsft", _F32, (m_total // 128,), both)
+    aqt_at, asft_at, ld_asft = None, None, 0
     if aqt is not None or asft is not None:
-        _dense(aqt, "aqt", _U8, (inter, m_total))
-        ld_asft = _scales(asft, "asft", _F32, (m_total // 128,), inter)
-    _call("dg_swiglu_bwd", _ptr(hq), _ptr(hsf), _ptr(dact), _ptr(m_indices), _ptr(dq), _ptr(dsf), _ptr(dqt), _ptr(dsft),
-          _ptr(aqt), _ptr(asft), m_total, inter, ld_hsf, ld_dact, ld_dsf, ld_dsft, ld_asft, _stream(dact))
+        aqt_at = _dense(aqt, "aqt", _U8, (inter, m_total))
+        asft_at, ld_asft = _scales(asft, "asft", _F32, (m_total // 128,), inter)
+    _check("dg_swiglu_bwd", _lib.dg_swiglu_bwd(
+        hq_at, hsf_at, dact_at, m_indices_at, dq_at, dsf_at, dqt_at, dsft_at, aqt_at, asft_at, m_total, inter, ld_hsf,
+        ld_dact, ld_dsf, ld_dsft, ld_asft, _stream(dact)))
     return dq, dsf, dqt, dsft, aqt, asft
 
 
@@ -379,15 +438,15 @@ def dg_requant_t(q, sf, m_indices, qt, sft):
     """Row-wise codes q [M][C], sf [C/128][ld] -> transposed codes qt [C][M] with
     one scale per column and 128 rows, sft [M/128][ld] (an operand of
     dg_k_grouped_nt); zeros at rows with m_indices < 0 (None: all in use)."""
-    _expect(q, "q", _U8, 2)
-    rows, cols = q.shape
-    _contig(q, "q")
-    _dense(qt, "qt", _U8, (cols, rows))
-    if m_indices is not None:
-        _dense(m_indices, "m_indices", _I32, (rows,))
-    ld_sf = _scales(sf, "sf", _F32, (cols // 128,), rows)
-    ld_sft = _scales(sft, "sft", _F32, (rows // 128,), cols)
-    _call("dg_requant_t", _ptr(q), _ptr(sf), _ptr(m_indices), _ptr(qt), _ptr(sft), rows, cols, ld_sf, ld_sft, _stream(q))
+    q_at, rows, cols, ld = _matrix(q, "q", _U8)
+    if ld != cols and q.numel():
+        _contig(q, "q")
+    qt_at = _dense(qt, "qt", _U8, (cols, rows))
+    m_indices_at = _dense_or_none(m_indices, "m_indices", _I32, (rows,))
+    sf_at, ld_sf = _scales(sf, "sf", _F32, (cols // 128,), rows)
+    sft_at, ld_sft = _scales(sft, "sft", _F32, (rows // 128,), cols)
+    _check("dg_requant_t", _lib.dg_requant_t(
+        q_at, sf_at, m_indices_at, qt_at, sft_at, rows, cols, ld_sf, ld_sft, _stream(q)))
     return qt, sft
 
 
