@@ -86,8 +86,9 @@ __device__ __forceinline__ uint4 encode16(const Values& at) {
 // magnitude tried on the host, 1.03e9 pairs; quotients below 2^-12 may differ
 // and have the code of zero).  The residual's order keeps the sign of a zero.
 // That needs residuals that float32 holds: tiles with s below 2^-90 (an all-zero
-// one among them) take the double-precision form.  (The latter for all: dispatch
-// of 32768 x 7168 131 us.)
+// one among them) take the double-precision form.  (That form for all takes as long
+// in the dispatch of 32768 x 7168, which waits for memory, but a quarter more
+// vector instructions.)
 __device__ __forceinline__ uint4 encode_bf16_tile(const Lane16& v, float& s) {
   const float amax = amax16([&](int i) { return v.at(i); });
   constexpr float kInv448 = 1.0f / 448.0f;
@@ -123,18 +124,32 @@ constexpr int kTileThreads = kBlockK * kBlockK / (8 * R);
 template <int R, int N = 1>
 struct TileLds {
   static constexpr int kGroups = kBlockK / R;
-  // Maximum of each column over each group of R rows; the padding keeps the two
-  // (four) parts of a column that are read together on different banks.
-  float partial[N][kGroups][kBlockK + 4];
-  float inv[N][kBlockK];
+  static constexpr int kParts = kTileThreads<R> / kBlockK;  // threads that share a column's maximum
+  // Maximum of each column over each group of R rows.  A thread writes 8 columns
+  // as two vectors, each into a half of the row of its own, so that 8 lanes write
+  // 128 consecutive bytes; the offsets of the halves and of every eighth group put
+  // what 32 lanes then read, 32 / kParts columns of kParts groups, on 32 different
+  // banks.
+  static constexpr int kHalf = kBlockK / 2 + 16 / kParts, kRow = kHalf + kBlockK / 2;
+  static __device__ __forceinline__ int partial_at(int group, int col) {
+    return group * kRow + (group >> 3) * (32 / kParts) + ((col >> 2) & 1) * kHalf + (col >> 3) * 4 + (col & 3);
+  }
+  static __device__ __forceinline__ int inv_at(int col) {
+    return ((col >> 2) & 1) * (kBlockK / 2) + (col >> 3) * 4 + (col & 3);
+  }
+  alignas(16) float partial[N][kGroups * kRow + 32];
+  alignas(16) float inv[N][kBlockK];
   alignas(16) uint8_t codes[N][kBlockK * kBlockK];
 };
 
-// Where byte 16 `chunk` of column `col` lies in TileLds::codes.  Lanes write
-// columns 8 apart and read 8 columns of 8 chunks: the exclusive-ors spread the
-// first over all banks and leave the second a permutation of 1 KB.
-__device__ __forceinline__ int codes_at(int col, int chunk) {
-  return (col ^ ((col >> 6) & 1)) * kBlockK + (chunk ^ ((col >> 3) & 7)) * 16;
+// Where the code of row `row` and column `col` lies in TileLds::codes.  32 lanes
+// write rows of columns 8 apart, 8 lanes read a column's 8 chunks of 16 bytes: the
+// exclusive-ors spread the first over all banks (bit 6 of the column picks which
+// half of a chunk holds its first 8 rows) and leave the second a permutation of
+// 128 bytes.  (The gated unit's backward, 32768 x 2048: 150 us with no conflicts
+// here or at the maxima, 153 with 2 and 4 lanes on a bank.)
+__device__ __forceinline__ int codes_at(int col, int row) {
+  return col * kBlockK + (((row >> 4) ^ ((col >> 3) & 7)) * 16) + ((row & 15) ^ ((col >> 6) * 8));
 }
 
 // Rows of the tile in use (index >= 0), the same in every wave: lane l looks at
@@ -238,7 +253,8 @@ struct ColumnsTo {
 // only behind a barrier that its last readers have passed.
 template <int R, int N>
 __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<R, N>& lds, const ColumnsTo (&to)[N]) {
-  constexpr int kParts = kTileThreads<R> / kBlockK;  // threads that share a column's maximum
+  using Lds = TileLds<R, N>;
+  constexpr int kParts = Lds::kParts;
   const int tid = threadIdx.x, group = tid >> 4, c0 = (tid & 15) * 8;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -249,9 +265,9 @@ __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<
 #pragma unroll
       for (int i = 2; i < R; i += 2) amax[c] = fmaxf(amax[c], fmaxf(fabsf(v[n][i][c]), fabsf(v[n][i + 1][c])));
     }
-    float4* at = reinterpret_cast<float4*>(&lds.partial[n][group][c0]);
-    at[0] = make_float4(amax[0], amax[1], amax[2], amax[3]);
-    at[1] = make_float4(amax[4], amax[5], amax[6], amax[7]);
+    float* at = lds.partial[n] + Lds::partial_at(group, c0);
+    *reinterpret_cast<float4*>(at) = make_float4(amax[0], amax[1], amax[2], amax[3]);
+    *reinterpret_cast<float4*>(at + Lds::kHalf) = make_float4(amax[4], amax[5], amax[6], amax[7]);
   }
   __syncthreads();
 #pragma unroll
@@ -259,12 +275,12 @@ __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<
     const int col = tid / kParts, part = tid % kParts;
     uint32_t u = 0;  // maxima are not negative: ordered like their bits
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u = umax(u, __float_as_uint(lds.partial[n][part * 8 + i][col]));
+    for (int i = 0; i < 8; ++i) u = umax(u, __float_as_uint(lds.partial[n][Lds::partial_at(part * 8 + i, col)]));
     u = umax(u, dpp<kXor1>(u));
     if (kParts == 4) u = umax(u, dpp<kXor2>(u));
     const TileScale t = tile_scale(__uint_as_float(u));
     if (part == 0) {
-      lds.inv[n][col] = t.inv;
+      lds.inv[n][Lds::inv_at(col)] = t.inv;
       if (to[n].q) to[n].sf[col] = t.s;
     }
   }
@@ -272,10 +288,11 @@ __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     float inv[8];
-    load_floats<8>(&lds.inv[n][c0], inv);
+    *reinterpret_cast<float4*>(inv) = *reinterpret_cast<const float4*>(lds.inv[n] + Lds::inv_at(c0));
+    *reinterpret_cast<float4*>(inv + 4) = *reinterpret_cast<const float4*>(lds.inv[n] + Lds::inv_at(c0 + 4));
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      uint8_t* at = lds.codes[n] + codes_at(c0 + c, group * R / 16) + group * R % 16;
+      uint8_t* at = lds.codes[n] + codes_at(c0 + c, group * R);
       const uint32_t lo = e4m3_x4(v[n][0][c] * inv[c], v[n][1][c] * inv[c], v[n][2][c] * inv[c], v[n][3][c] * inv[c]);
       if constexpr (R == 8) {
         const uint32_t hi = e4m3_x4(v[n][4][c] * inv[c], v[n][5][c] * inv[c], v[n][6][c] * inv[c], v[n][7][c] * inv[c]);
@@ -293,9 +310,11 @@ __device__ __forceinline__ void tile_columns(const float (&v)[N][R][8], TileLds<
     if (!to[n].q) continue;
 #pragma unroll
     for (int i = 0; i < kBlockK / kColumns; ++i) {
-      const int col = i * kColumns + (tid >> 3), chunk = tid & 7;
-      store_streaming(to[n].q + (int64_t)col * to[n].ldq + chunk * 16,
-                      *reinterpret_cast<const uint4*>(lds.codes[n] + codes_at(col, chunk)));
+      const int col = i * kColumns + (tid >> 3), row = (tid & 7) * 16;
+      const bool swapped = i * kColumns >= 64;
+      const uint4 w = *reinterpret_cast<const uint4*>(lds.codes[n] + (codes_at(col, row) & ~15));
+      store_streaming(to[n].q + (int64_t)col * to[n].ldq + row,
+                      swapped ? make_uint4(w.z, w.w, w.x, w.y) : w);
     }
   }
 }
