@@ -16,7 +16,8 @@ namespace {
 // of its expert in the blocks before, in the waves before, and in the lanes
 // before, which a ballot for each bit of the expert's number tells.  Up to 4096
 // entries one workgroup does it all in one launch (1024 entries of 32 experts:
-// 4.7 us, against 1.3 + 4.7 in two launches).
+// 4.7 us, against 1.3 + 4.7 in two launches).  Both are a chain of reads and
+// barriers, not a stream: 131072 entries of 4 experts take 3.0 + 4.8 us for 2 MB.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kOnePlanEntries = 4096;
@@ -167,7 +168,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
 
 // Row-wise gather and quantise, the mapping of the plain activation
 // quantiser: 8 lanes own a 128-value tile, a wave owns 8 tiles of a row and
-// U rows at a time.
+// U rows at a time, so that the gathered loads of U rows are in flight together.
+// A token's rows are in different groups, far apart in the walk, so each row of
+// the result is a read of its own: 32768 rows x 7168 of 16384 tokens read 0.45 GB
+// and write 0.23 in 114 us (5.9 TB/s).  Reads alone take 86 us, writes alone 45,
+// the arithmetic 57.  Rows put in token order, so that a token's second read finds
+// it in an L2, bring 109 at best and need a sort; 16 lanes a tile 135 and more.
 constexpr int kTilesPerWave = 8;
 constexpr int kRowWaves = 4;
 
@@ -214,7 +220,10 @@ __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams
 
 // ---------------------------------------------------------------- combine --
 
-// Workgroup (x, t): 2048 columns of token t, 8 a thread.
+// Workgroup (t, y): 2048 columns of token t, 8 a thread: one pass over the rows,
+// sums in float32 registers, the only rounding at the end.  Bound by the reads:
+// 32110 rows x 7168 into 4096 tokens in 95 us, 0.46 GB read and 0.06 written
+// (5.5 TB/s).
 constexpr int kCombineThreads = 256;
 
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams p) {
@@ -243,7 +252,13 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
   *reinterpret_cast<uint4*>(p.y + t * p.ld_y + col) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Workgroup: one 128 x 128 tile of the expert rows.
+// Workgroup: one 128 x 128 tile of the expert rows.  dy and d are read once for
+// all three results: the products go from registers to row codes and, through
+// shared memory, to column codes; the rows' dot products over this tile's columns
+// go to the workspace, summed in a fixed order by the next kernel (an atomic sum
+// would differ from run to run).  Bound by memory: 32768 rows x 7168 move 0.74 GB
+// in and 0.47 out in 215 to 260 us (5.6 to 4.6 TB/s), by where the five matrices
+// lie; tiles in row order, in panels, or sorted by token change nothing or lose.
 __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwdParams p) {
   __shared__ TileLds<8> lds;
   const TileAt tile = tile_of_workgroup(p.m_total / kBlockK);
@@ -295,7 +310,7 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
 
 // Workgroup x: the dot products of rows [64 x, 64 x + 64), each wave every fourth
 // tile's, added into the rows' entries; and zeros for those of entries
-// [256 x, 256 x + 256) that no row is of.
+// [256 x, 256 x + 256) that no row is of.  (32768 rows x 56 tiles: 5.9 us.)
 __global__ __launch_bounds__(256) void combine_dweights_kernel(CombineBwdParams p) {
   __shared__ float part[4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -344,7 +359,11 @@ hipError_t launch_plan(const PlanParams& params, hipStream_t stream) {
 hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t stream) {
   const int gx = (p.cols / kBlockK + kTilesPerWave - 1) / kTilesPerWave;
   const int64_t total = (int64_t)p.groups * p.rows;
-  const int u = total >= 16384 ? 4 : total >= 2048 ? 2 : 1;
+  // Tall layouts are streams, which four rows of a wave at a time and streaming
+  // stores suit (32768 x 7168: 115 us, and 124 row by row with plain stores); short
+  // ones wait for their reads, which more waves share (128 tokens in 32 groups of
+  // 128 rows: 4.8 us, and 5.7 by four; 8192 rows: 21.9 and 22.8).
+  const int u = total >= 16384 ? 4 : 1;
   int64_t gy = (16384 / kRowWaves + gx - 1) / gx;
   const int64_t need = (total + kRowWaves * u - 1) / (kRowWaves * u);
   if (gy > need) gy = need;
@@ -352,11 +371,9 @@ hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t strea
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
   if (pow2) {
     if (u == 4) go(dispatch_kernel<true, 4>);
-    else if (u == 2) go(dispatch_kernel<true, 2>);
     else go(dispatch_kernel<true, 1>);
   } else {
     if (u == 4) go(dispatch_kernel<false, 4>);
-    else if (u == 2) go(dispatch_kernel<false, 2>);
     else go(dispatch_kernel<false, 1>);
   }
   return hipGetLastError();

@@ -175,7 +175,7 @@ __device__ __forceinline__ TileUse tile_use(const int32_t* index) {
 // that run one after another on one XCD (every eighth) take a contiguous eighth
 // of the tiles, row tiles fastest: they write neighbouring pieces of the same
 // columns through one L2 (requantising 32768 x 7168: 92 us against 98 in plain
-// order).
+// order, 118 and more in panels of rows; 83 with streaming stores).
 struct TileAt {
   int row, col;
 };
