@@ -38,7 +38,9 @@ struct RouteParams {
   int64_t ld, ld_d;
   int sigmoid;  // 0: softmax
   int groups, topk_groups, group_top;
-  int per_group, group_shift;  // experts of a group; log2 of its lanes, or -1 (set by the launch)
+  // Set by the launch: experts of a group, log2 of its lanes, whether those hold its experts.
+  int per_group, group_shift, group_whole;
+  Divisor by_group;
   int renormalize;
   float scale;
 };

@@ -6,9 +6,10 @@
 // order of lanes and registers is the order of the experts (ties), and every
 // reduction stays in registers (row operations and readlane, no shared memory).
 // A token is read once.  What bounds the choice is the issue of vector
-// instructions, about 410 a token of 256 experts in groups (19 a round of the
-// top-k, 11 a sigmoid): 32768 tokens in 21.5 us, 59 us with shuffles for the row
-// operations and 64-bit keys.  The gradient is bound by what it writes: 10.9 us.
+// instructions, 378 a token of 256 experts in groups (17 a round of the top-k, 11
+// a sigmoid): 32768 tokens in 21.6 us, 59 us with shuffles for the row operations
+// and 64-bit keys.  The gradient is bound by memory and by its start: it writes 34
+// MB and reads the lines of the chosen logits in 10.8 us.
 
 #include "dg_math.h"
 #include "dg_moe_internal.h"
@@ -32,9 +33,11 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
 };
 
 // The lane's V logits, -inf past the last expert.  VEC: rows and their length
-// allow whole vectors (decided on the host).
+// allow whole vectors (decided on the host); otherwise the wave reads them in
+// order and hands them out through its 64 V words of shared memory (32768 rows of
+// 500: 41 us, 60 with each lane reading its own).
 template <bool VEC, typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int experts, int lane, float (&x)[V]) {
+__device__ __forceinline__ void load_row(const T* row, int experts, int lane, float* lds, float (&x)[V]) {
   const int e0 = lane * V;
   if constexpr (VEC) {
 #pragma unroll
@@ -44,9 +47,20 @@ __device__ __forceinline__ void load_row(const T* row, int experts, int lane, fl
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = widen(in.v[i]);
     }
+  } else if constexpr (V == 1) {
+    x[0] = lane < experts ? widen(row[lane]) : -INFINITY;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = e0 + i < experts ? widen(row[e0 + i]) : -INFINITY;
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 64 + lane;
+      x[i] = e < experts ? widen(row[e]) : -INFINITY;
+    }
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) lds[i * 64 + lane] = x[i];
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = lds[e0 + i];
   }
 }
 
@@ -101,8 +115,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
   float x[V], s[V], bias[V];
   uint32_t key[V];  // 0: cannot be chosen
   int idx[V];
-  load_row<VEC>(static_cast<const T*>(p.logits) + t * p.ld, p.experts, lane, x);
-  if constexpr (BIAS) load_row<VEC>(p.bias, p.experts, lane, bias);
+  load_row<VEC>(static_cast<const T*>(p.logits) + t * p.ld, p.experts, lane, lds[wave], x);
+  if constexpr (BIAS) load_row<VEC>(p.bias, p.experts, lane, lds[wave], bias);
   scores<V>(x, s, p.sigmoid != 0);
 #pragma unroll
   for (int i = 0; i < V; ++i) lds[wave][lane * V + i] = s[i];
@@ -115,40 +129,39 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
   }
 
   if constexpr (GROUPS) {
-    // Two largest keys of each group: in groups of 2^n whole lanes by row
-    // operations, otherwise lane g walks group g in shared memory (256 experts in
-    // 8 groups, 32768 tokens: 21.5 us, and 32.6 by the walk).
+    // Two largest keys of each group by its 2^group_shift lanes: those that hold
+    // the group's experts where that many lanes hold them and no others, otherwise
+    // an equal share of the wave, which looks at them in shared memory (256 experts
+    // in 8 groups, 32768 tokens: 21.6 us, and 24.2 by shared memory).
     uint32_t a = 0, b = 0;
-    const bool whole = p.group_shift >= 0;
-    const int mine = whole ? lane >> p.group_shift : lane;  // the group this lane holds the score of
-    if (whole) {
+    const int lanes = 1 << p.group_shift, sub = lane & (lanes - 1);
+    const int mine = lane >> p.group_shift;  // the lane's group
+    if (p.group_whole) {
 #pragma unroll
       for (int i = 0; i < V; ++i) merge_top2(a, b, key[i], 0u);
-      if (p.group_shift > 0) merge_top2(a, b, dpp<kXor1>(a), dpp<kXor1>(b));
-      if (p.group_shift > 1) merge_top2(a, b, dpp<kXor2>(a), dpp<kXor2>(b));
-      if (p.group_shift > 2) merge_top2(a, b, dpp<kHalfMirror>(a), dpp<kHalfMirror>(b));
-      if (p.group_shift > 3) merge_top2(a, b, dpp<kRowMirror>(a), dpp<kRowMirror>(b));
-      if (p.group_shift > 4) merge_top2(a, b, __shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
     } else {
       __shared__ uint32_t keys[kWaves][64 * V];
 #pragma unroll
       for (int i = 0; i < V; ++i) keys[wave][lane * V + i] = key[i];
       wave_fence();
-      if (lane < p.groups)
-        for (int i = 0; i < p.per_group; ++i) merge_top2(a, b, keys[wave][lane * p.per_group + i], 0u);
+      if (mine < p.groups)
+        for (int i = sub; i < p.per_group; i += lanes) merge_top2(a, b, keys[wave][mine * p.per_group + i], 0u);
     }
+    if (p.group_shift > 0) merge_top2(a, b, dpp<kXor1>(a), dpp<kXor1>(b));
+    if (p.group_shift > 1) merge_top2(a, b, dpp<kXor2>(a), dpp<kXor2>(b));
+    if (p.group_shift > 2) merge_top2(a, b, dpp<kHalfMirror>(a), dpp<kHalfMirror>(b));
+    if (p.group_shift > 3) merge_top2(a, b, dpp<kRowMirror>(a), dpp<kRowMirror>(b));
+    if (p.group_shift > 4) merge_top2(a, b, __shfl_xor(a, 16, 64), __shfl_xor(b, 16, 64));
     const uint32_t score = a == 0u ? 0u : p.group_top == 2 && b != 0u ? order_of(of_order(a) + of_order(b)) : a;
     int before = 0;  // groups that come first
-    if (p.groups * p.groups <= 64 && whole && p.groups << p.group_shift == 64) {
-      // The lanes of a group each look at one other group (23.1 us with the loop
-      // below).
-      const int other_group = lane & ((1 << p.group_shift) - 1);
-      const uint32_t other = (uint32_t)__shfl((int)score, other_group << p.group_shift, 64);
-      const bool first = other_group < p.groups && (other > score || (other == score && other_group < mine));
-      before = __popcll((__ballot(first) >> (mine << p.group_shift)) & ((1ull << (1 << p.group_shift)) - 1ull));
+    if (p.groups <= lanes) {
+      // Each lane of a group looks at one other group (23.1 us with the loop below).
+      const uint32_t other = (uint32_t)__shfl((int)score, sub << p.group_shift, 64);
+      const bool first = sub < p.groups && (other > score || (other == score && sub < mine));
+      before = __popcll((__ballot(first) >> (lane - sub)) & ((1ull << lanes) - 1ull));
     } else {
       for (int g = 0; g < p.groups; ++g) {
-        const uint32_t other = lane_value(score, whole ? g << p.group_shift : g);
+        const uint32_t other = lane_value(score, g << p.group_shift);
         before += other > score || (other == score && g < mine);
       }
     }
@@ -157,9 +170,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       bool in = stays;
-      if (!whole) {
-        const int g = (lane * V + i) / p.per_group;
-        in = g < 64 && ((kept >> g) & 1);
+      if (!p.group_whole) {
+        const int g = (int)divided(lane * V + i, p.by_group);
+        in = g < p.groups && ((kept >> (g << p.group_shift)) & 1);
       }
       // Without a bias the groups go by scores, the experts by their logits.
       const uint32_t k = BIAS ? key[i] : order_of(x[i]);
@@ -192,10 +205,11 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
   for (int j = 0; j < p.topk; ++j) {
     const uint32_t best = wave_max(key[0]);
     if (best == 0u) break;
-    const int from = __builtin_ctzll(__ballot(key[0] == best));
+    const uint64_t heads = __ballot(key[0] == best);
+    const int from = __builtin_ctzll(heads);
     const int e = from * V + (__builtin_amdgcn_readlane((int)order, from) & 15);
-    id = lane == j ? e : id;
-    const bool pop = lane == from;
+    id = __builtin_amdgcn_inverse_ballot_w64(1ull << j) ? e : id;
+    const bool pop = __builtin_amdgcn_inverse_ballot_w64(heads & -heads);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t same = key[i], next = i + 1 < V ? key[i + 1] : 0u;
@@ -235,7 +249,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   if constexpr (SIGMOID) {
     if (id >= 0) sel = score_sigmoid(widen(row[id]));
   } else {
-    load_row<VEC>(row, p.experts, lane, x);
+    load_row<VEC>(row, p.experts, lane, lds[wave], x);
     scores<V>(x, s, false);
 #pragma unroll
     for (int i = 0; i < V; ++i) mine[i] = s[i];
@@ -254,16 +268,25 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   if (id >= 0) lds[wave][id] = SIGMOID ? g * sel * (1.0f - sel) : g;
   wave_fence();
   const float mean = SIGMOID ? 0.0f : wave_sum(g * sel);
-  Pack<T, V> out;
+  T* to = static_cast<T*>(p.dlogits) + t * p.ld_d;
+  float out[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) narrow(out.v[i], SIGMOID ? mine[i] : s[i] * (mine[i] - mean));
-  T* to = static_cast<T*>(p.dlogits) + t * p.ld_d + lane * V;
+  for (int i = 0; i < V; ++i) out[i] = SIGMOID ? mine[i] : s[i] * (mine[i] - mean);
   if constexpr (VEC) {
-    if (lane * V < p.experts) *reinterpret_cast<Pack<T, V>*>(to) = out;
-  } else {
+    Pack<T, V> pack;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i < p.experts) to[i] = out.v[i];
+    for (int i = 0; i < V; ++i) narrow(pack.v[i], out[i]);
+    if (lane * V < p.experts) *reinterpret_cast<Pack<T, V>*>(to + lane * V) = pack;
+  } else {
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[i] = out[i];
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 64 + lane;
+      if (e < p.experts) narrow(to[e], lds[wave][e]);
+    }
   }
 }
 
@@ -279,15 +302,17 @@ void go(const RouteParams& p, bool bwd, hipStream_t stream) {
   else hipLaunchKernelGGL((route_bwd_kernel<VEC, T, V, false>), grid, block, 0, stream, p);
 }
 
-// Whole vectors: no ragged last lane, and every row starts on a vector (21.5 us
-// against 23.5 with single elements).
+// Whole vectors: no ragged last lane, and every row starts on a vector (32768 rows
+// of 256: 21.4 us, and 22.8 through shared memory).
 template <typename T, int V>
 void go(RouteParams p, bool bwd, hipStream_t stream) {
-  p.group_shift = -1;
-  if (!bwd) {
+  if (!bwd && p.groups > 1) {
     p.per_group = p.experts / p.groups;
+    p.by_group = divisor(p.per_group);
+    p.group_shift = 6;
+    while (p.groups > 64 >> p.group_shift) --p.group_shift;
     for (int shift = 0; shift < 6; ++shift)
-      if (p.per_group == V << shift) p.group_shift = shift;
+      if (p.per_group == V << shift) p.group_shift = shift, p.group_whole = 1;
   }
   constexpr size_t kAlign = alignof(Pack<T, V>);
   auto fits = [&](const void* at, int64_t ld) {

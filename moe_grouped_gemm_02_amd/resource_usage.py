@@ -20,7 +20,7 @@ sys.path.insert(0, os.path.dirname(HERE))
 from moe_grouped_gemm_02_amd import build as B  # noqa: E402
 
 CXXFILT = "c++filt"
-KERNEL_SOURCES = ["dg_gemm.hip", "dg_quant.hip"]
+KERNEL_SOURCES = ["dg_gemm.hip", "dg_quant.hip", "dg_route.hip", "dg_exchange.hip", "dg_ckpt.hip"]
 FIELDS = [("VGPRs", "VGPRs"), ("AGPRs", "AGPRs"), ("TotalSGPRs", "SGPRs"),
           ("ScratchSize [bytes/lane]", "scratch B/lane"), ("VGPRs Spill", "VGPR spill"),
           ("SGPRs Spill", "SGPR spill"), ("LDS Size [bytes/block]", "static LDS B"),
