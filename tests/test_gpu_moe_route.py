@@ -218,3 +218,20 @@ def test_many_tokens_and_no_tokens():
     ref = x.sort(dim=1, descending=True, stable=True).indices[:, :2]
     assert torch.equal(ids.long(), ref)
     dg.dg_moe_route(x[:0], ids[:0], w[:0])
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("experts,groups,keep", [(34, 2, 1), (92, 4, 2), (184, 8, 3), (192, 6, 2), (500, 4, 2), (1016, 8, 4),
+                                                 (96, 32, 7), (62, 31, 9), (1024, 64, 11)])
+def test_groups_of_any_size(experts, groups, keep, bias):
+    """Groups that fill their lanes and groups that do not, few and many, some with every expert masked."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts + groups)
+    x = _bf(1.5 * rng.standard_normal((67, experts)))
+    x[:20, :experts // groups] = -np.inf
+    x[20:40][rng.random((20, experts)) < 0.5] = -np.inf
+    kw = dict(score="sigmoid", expert_groups=groups, topk_groups=keep, scale=2.5)
+    if bias:
+        kw["bias"] = (0.2 * rng.standard_normal(experts)).astype(np.float32)
+    for group_top in (1, 2):
+        _check(dg, x, min(8, keep * (experts // groups)), False, 0, dict(kw, group_top=group_top), gap=1e-6)
