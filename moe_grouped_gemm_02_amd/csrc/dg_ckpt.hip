@@ -220,12 +220,15 @@ __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParam
 
 hipError_t launch_swiglu_quant(const SwigluParams& p, bool pow2, hipStream_t stream) {
   const int gx = (p.inter / kBlockK + kTilesPerWave - 1) / kTilesPerWave;
-  // Up to 4096 workgroups in all; each group its share of them.  A short masked
-  // layout has 1024: most of its rows are not in use when the batch is small, and
-  // workgroups that find nothing to do cost more than they bring (32 groups of 128
-  // rows x 2048, 4 % in use: 4.4 us against 6.3; all in use: a call in 8.8 against
-  // 8.5; 1024 rows in each group: 55.6 against 47.5).
-  const int64_t most = p.masked_m && (int64_t)p.groups * p.rows * p.inter <= (int64_t)16 << 20 ? 1024 : 4096;
+  // Up to 16384 workgroups in all, most rows a wave of their own (32768 x 2048: 79
+  // us, and 89.5 with 4096); each group its share of them.  A masked layout, whose
+  // rows are mostly not in use when the batch is small, has fewer, since workgroups
+  // that find nothing to do cost more than they bring: 1024 of a short one (32
+  // groups of 128 rows x 2048, 4 % in use: 4.4 us against 6.3 with 4096; all in use:
+  // a call in 8.8 against 8.5), 8192 of a tall one (32 groups of 1024 rows, 4 % in
+  // use: a call in 7.6, and 10.2 with 16384; all in use: 44.3 and 42.9).
+  const bool short_layout = (int64_t)p.groups * p.rows * p.inter <= (int64_t)16 << 20;
+  const int64_t most = !p.masked_m ? 16384 : short_layout ? 1024 : 8192;
   const int64_t share = (most + (int64_t)gx * p.groups - 1) / ((int64_t)gx * p.groups);
   const int64_t need = ((int64_t)p.rows + kRowWaves - 1) / kRowWaves;
   const dim3 grid(gx, (unsigned)(need < share ? need : share), p.groups), block(64 * kRowWaves);

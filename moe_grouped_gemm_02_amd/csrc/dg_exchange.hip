@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
   for (int64_t r = (int64_t)blockIdx.x * kPlanThreads + tid; r < p.layout_rows; r += (int64_t)gridDim.x * kPlanThreads) {
     int lo = 0;  // the last group that starts at or before row r
     if (p.masked) {
-      lo = (int)((uint32_t)r / (uint32_t)p.m_max);
+      lo = (int)divided((uint32_t)r, p.by_m_max);
     } else {
       int hi = p.groups;
       while (hi - lo > 1) {
@@ -168,50 +168,52 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
 
 // Row-wise gather and quantise, the mapping of the plain activation
 // quantiser: 8 lanes own a 128-value tile, a wave owns 8 tiles of a row and
-// U rows at a time, so that the gathered loads of U rows are in flight together.
+// ROWS rows at a time, so that their gathered loads are in flight together; which
+// rows and tokens is the same for the whole wave and kept in scalar registers.
 // A token's rows are in different groups, far apart in the walk, so each row of
 // the result is a read of its own: 32768 rows x 7168 of 16384 tokens read 0.45 GB
-// and write 0.23 in 114 us (5.9 TB/s).  Reads alone take 86 us, writes alone 45,
-// the arithmetic 57.  Rows put in token order, so that a token's second read finds
-// it in an L2, bring 109 at best and need a sort; 16 lanes a tile 135 and more.
+// and write 0.23 in 107 us (6.3 TB/s).  The reads alone take 86.  Rows put in token
+// order, so that a token's second read finds it in an L2, gained 5 % and need a
+// sort; 16 lanes a tile lost (135 and more).
 constexpr int kTilesPerWave = 8;
 constexpr int kRowWaves = 4;
 
-template <bool POW2, int U>
+template <bool POW2, int ROWS>
 __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams p) {
   const int tiles_per_row = p.cols / kBlockK;
-  const int64_t total_rows = (int64_t)p.groups * p.rows;
-  const uint32_t entries = (uint32_t)(p.tokens * p.topk);
-  const int sub = threadIdx.x & 7;
-  const int j = blockIdx.x * kTilesPerWave + ((threadIdx.x & 63) >> 3);
-  const int wave = threadIdx.x >> 6;
-  if (j >= tiles_per_row) return;
-  const int64_t step = (int64_t)gridDim.y * kRowWaves * U;
-  for (int64_t r0 = ((int64_t)blockIdx.y * kRowWaves + wave) * U; r0 < total_rows; r0 += step) {
-    Lane16 in[U];
-    bool live[U];
+  const uint32_t total_rows = (uint32_t)p.groups * (uint32_t)p.rows, entries = (uint32_t)(p.tokens * p.topk);
+  const int lane = threadIdx.x & 63, sub = lane & 7;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = blockIdx.x * kTilesPerWave + (lane >> 3);
+  const bool in = j < tiles_per_row;
+  const int col = j * kBlockK + sub * 16;
+  const uint32_t step = gridDim.y * kRowWaves * ROWS;
+  for (uint32_t r0 = (blockIdx.y * kRowWaves + wave) * ROWS; r0 < total_rows; r0 += step) {
+    uint32_t entry = ~0u;
+    if (lane < ROWS && r0 + lane < total_rows) entry = (uint32_t)p.src[r0 + lane];
+    const uint64_t rows = __ballot(entry < entries);
+    if (rows == 0) continue;
+    Lane16 x[ROWS];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t e = r0 + u < total_rows ? (uint32_t)p.src[r0 + u] : ~0u;
-      live[u] = e < entries;
-      if (live[u]) in[u] = load16(p.x + (int64_t)(divided(e, p.by_topk)) * p.ld_x + j * kBlockK + sub * 16);
+    for (int u = 0; u < ROWS; ++u) {
+      const uint32_t token = divided(lane_value(entry, u), p.by_topk);
+      if (in && ((rows >> u) & 1)) x[u] = load16(p.x + (int64_t)token * p.ld_x + col);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!live[u]) continue;
-      const int64_t gr = r0 + u;
-      const int64_t g = gr / p.rows, r = gr - g * p.rows;
-      const int64_t sf_at = (g * tiles_per_row + j) * p.ld_sf + r;
-      uint4* to = reinterpret_cast<uint4*>(p.q + gr * p.cols + j * kBlockK + sub * 16);
+    for (int u = 0; u < ROWS; ++u) {
+      if (!in || !((rows >> u) & 1)) continue;
+      const uint32_t row = r0 + u, g = divided(row, p.by_rows), r = row - g * (uint32_t)p.rows;
+      const int64_t sf_at = ((int64_t)g * tiles_per_row + j) * p.ld_sf + r;
+      uint4* to = reinterpret_cast<uint4*>(p.q + (int64_t)row * p.cols + col);
       if constexpr (POW2) {
         uint32_t e;
-        const uint4 q = encode_bf16_tile_pow2(in[u], e);
-        store<U == 4>(to, q);
+        const uint4 q = encode_bf16_tile_pow2(x[u], e);
+        store<ROWS == 4>(to, q);
         if (sub == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
       } else {
         float s;
-        const uint4 q = encode_bf16_tile(in[u], s);
-        store<U == 4>(to, q);
+        const uint4 q = encode_bf16_tile(x[u], s);
+        store<ROWS == 4>(to, q);
         if (sub == 0) static_cast<float*>(p.sf)[sf_at] = s;
       }
     }
@@ -362,18 +364,20 @@ hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t strea
   // Tall layouts are streams, which four rows of a wave at a time and streaming
   // stores suit (32768 x 7168: 115 us, and 124 row by row with plain stores); short
   // ones wait for their reads, which more waves share (128 tokens in 32 groups of
-  // 128 rows: 4.8 us, and 5.7 by four; 8192 rows: 21.9 and 22.8).
-  const int u = total >= 16384 ? 4 : 1;
-  int64_t gy = (16384 / kRowWaves + gx - 1) / gx;
-  const int64_t need = (total + kRowWaves * u - 1) / (kRowWaves * u);
+  // 128 rows: 4.8 us, and 5.7 by four; 8192 rows: a call in 21.9 and 22.8).
+  const int rows = total >= 16384 ? 4 : 1;
+  // Tall: most waves make one trip (107 us, 114 with up to four trips).  Short: up
+  // to two (8192 rows: a call in 23.6, 24.3 with one).
+  int64_t gy = ((rows == 4 ? 65536 : 16384) / kRowWaves + gx - 1) / gx;
+  const int64_t need = (total + kRowWaves * rows - 1) / (kRowWaves * rows);
   if (gy > need) gy = need;
   const dim3 grid(gx, (unsigned)(gy < 1 ? 1 : gy)), block(64 * kRowWaves);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, p); };
   if (pow2) {
-    if (u == 4) go(dispatch_kernel<true, 4>);
+    if (rows == 4) go(dispatch_kernel<true, 4>);
     else go(dispatch_kernel<true, 1>);
   } else {
-    if (u == 4) go(dispatch_kernel<false, 4>);
+    if (rows == 4) go(dispatch_kernel<false, 4>);
     else go(dispatch_kernel<false, 1>);
   }
   return hipGetLastError();

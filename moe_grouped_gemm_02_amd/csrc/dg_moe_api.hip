@@ -147,6 +147,7 @@ int plan_impl(const int32_t* ids, int32_t* rows, int32_t* src, int32_t* m_indice
   p.hist = static_cast<int32_t*>(workspace);
   p.entries = tokens * topk, p.first = first_expert, p.groups = num_groups;
   p.masked = masked, p.m_max = m_max, p.layout_rows = layout_rows;
+  p.by_m_max = dg::divisor(m_max);
   return launched(dg::launch_plan(p, static_cast<hipStream_t>(stream)), "plan");
 }
 
@@ -161,7 +162,8 @@ int dispatch_impl(const uint16_t* x, const int32_t* src, uint8_t* q, void* sf, i
   if (!x || !src || !q || !sf) return fail(DG_ERR_INVALID_VALUE, "null pointer argument");
   if (!aligned16(x) || !aligned16(q) || !aligned16(sf) || !aligned(src, 4))
     return fail(DG_ERR_MISALIGNED, "x, q and sf must be 16-byte aligned, src 4-byte aligned");
-  const dg::DispatchParams p{x, src, q, sf, tokens, topk, cols, rows, num_groups, ld_x, ld_sf, dg::divisor(topk)};
+  const dg::DispatchParams p{x, src, q, sf, tokens, topk, cols, rows, num_groups, ld_x, ld_sf,
+                             dg::divisor(topk), dg::divisor(rows)};
   return launched(dg::launch_dispatch(p, pow2, static_cast<hipStream_t>(stream)), "dispatch");
 }
 

@@ -60,6 +60,7 @@ struct PlanParams {
   int first, groups;
   int masked, m_max;   // masked layout and its rows per group
   int layout_rows;
+  Divisor by_m_max;  // masked only
 };
 size_t plan_workspace_bytes(int64_t entries, int groups);
 hipError_t launch_plan(const PlanParams& p, hipStream_t stream);
@@ -71,7 +72,7 @@ struct DispatchParams {
   void* sf;
   int tokens, topk, cols, rows, groups;
   int64_t ld_x, ld_sf;
-  Divisor by_topk;
+  Divisor by_topk, by_rows;
 };
 hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t stream);
 
