@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kTileThreads<4>, 2) void swiglu_bwd_kernel(SwigluBw
 // and writes 0.23 in 83 us (5.6 TB/s).
 __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParams p) {
   __shared__ TileLds<8> lds;
-  const TileAt tile = tile_of_workgroup(p.rows / kBlockK);
+  const TileAt tile = tile_of_workgroup(p.rows / kBlockK, p.cols / kBlockK);
   const int64_t row0 = (int64_t)tile.row * kBlockK;
   const int col0 = tile.col * kBlockK;
   const int tid = threadIdx.x, r0 = (tid >> 4) * 8, c0 = (tid & 15) * 8;

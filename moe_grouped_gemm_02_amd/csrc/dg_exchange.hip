@@ -254,6 +254,32 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
   *reinterpret_cast<uint4*>(p.y + t * p.ld_y + col) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// 8 columns of dy and d multiplied and added to a sum.
+__device__ __forceinline__ float add_dot8(uint4 a, uint4 b, float sum) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    sum = fmaf(bf16_bits_to_f32(x[c] & 0xFFFFu), bf16_bits_to_f32(y[c] & 0xFFFFu), sum);
+    sum = fmaf(bf16_bits_to_f32(x[c] >> 16), bf16_bits_to_f32(y[c] >> 16), sum);
+  }
+  return sum;
+}
+
+// The weight's gradient of entry e by one wave.
+__device__ __forceinline__ void dweight_of_entry(const CombineBwdParams& p, int e) {
+  const int lane = threadIdx.x & 63;
+  const int row = p.rows[e];
+  float sum = 0.0f;
+  if (row >= 0 && row < p.m_total && p.src[row] == e) {
+    const uint16_t* dy = p.dy + (int64_t)divided((uint32_t)e, p.by_topk) * p.ld_dy;
+    const uint16_t* d = p.d + (int64_t)row * p.ld_d;
+    for (int c = lane * 8; c < p.cols; c += 64 * 8)
+      sum = add_dot8(*reinterpret_cast<const uint4*>(dy + c), *reinterpret_cast<const uint4*>(d + c), sum);
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) p.dweights[e] = sum;
+}
+
 // Workgroup: one 128 x 128 tile of the expert rows.  dy and d are read once for
 // all three results: the products go from registers to row codes and, through
 // shared memory, to column codes; the rows' dot products over this tile's columns
@@ -261,9 +287,22 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams 
 // would differ from run to run).  Bound by memory: 32768 rows x 7168 move 0.74 GB
 // in and 0.47 out in 215 to 260 us (5.6 to 4.6 TB/s), by where the five matrices
 // lie; tiles in row order, in panels, or sorted by token change nothing or lose.
+//
+// APART: workgroups past the tiles sum the weights' gradient of four entries each,
+// reading their rows again, and no second kernel is needed.
+template <bool APART>
 __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwdParams p) {
   __shared__ TileLds<8> lds;
-  const TileAt tile = tile_of_workgroup(p.m_total / kBlockK);
+  const int row_tiles = p.m_total / kBlockK, column_tiles = p.cols / kBlockK;
+  if constexpr (APART) {
+    const int past = (int)blockIdx.x - row_tiles * column_tiles;
+    if (past >= 0) {
+      const int e = past * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      if (e < p.tokens * p.topk) dweight_of_entry(p, e);
+      return;
+    }
+  }
+  const TileAt tile = tile_of_workgroup(row_tiles, column_tiles);
   const int64_t row0 = (int64_t)tile.row * kBlockK;
   const int col0 = tile.col * kBlockK;
   const int tid = threadIdx.x, r0 = (tid >> 4) * 8, i16 = tid & 15, c0 = i16 * 8;
@@ -283,27 +322,25 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
     if (e < entries) {
       live |= 1u << i;
       a[i] = *reinterpret_cast<const uint4*>(p.dy + (int64_t)(divided(e, p.by_topk)) * p.ld_dy + col0 + c0);
-      b[i] = load_streaming4(p.d + r * p.ld_d + col0 + c0);
+      if (!APART) b[i] = load_streaming4(p.d + r * p.ld_d + col0 + c0);
       w[i] = p.weights[e];
     }
   }
   float mine = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-    float dot = 0.0f;
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float x0 = bf16_bits_to_f32(x[c] & 0xFFFFu), x1 = bf16_bits_to_f32(x[c] >> 16);
-      dot = fmaf(x0, bf16_bits_to_f32(y[c] & 0xFFFFu), dot);
-      dot = fmaf(x1, bf16_bits_to_f32(y[c] >> 16), dot);
-      v[i][2 * c] = w[i] * x0;
-      v[i][2 * c + 1] = w[i] * x1;
+      v[i][2 * c] = w[i] * bf16_bits_to_f32(x[c] & 0xFFFFu);
+      v[i][2 * c + 1] = w[i] * bf16_bits_to_f32(x[c] >> 16);
     }
-    dot = row_sum(dot);
-    mine = i16 == i ? dot : mine;
+    if constexpr (!APART) {
+      const float dot = row_sum(add_dot8(a[i], b[i], 0.0f));
+      mine = i16 == i ? dot : mine;
+    }
   }
-  if (i16 < 8 && ((live >> i16) & 1)) p.dots[tile.col * (int64_t)p.m_total + row0 + r0 + i16] = mine;
+  if (!APART && i16 < 8 && ((live >> i16) & 1)) p.dots[tile.col * (int64_t)p.m_total + row0 + r0 + i16] = mine;
   tile_rows<8>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + tile.col * p.ld_dsf + row0, live);
   if (!p.dqt) return;
   const ColumnsTo to[1] = {{p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, p.dsft + (int64_t)tile.row * p.ld_dsft + col0}};
@@ -391,8 +428,17 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
 
 hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream) {
   const int tiles = p.m_total / kBlockK * (p.cols / kBlockK);
-  if (tiles > 0) hipLaunchKernelGGL(combine_bwd_kernel, dim3(tiles), dim3(kTileThreads<8>), 0, stream, p);
   const int64_t entries = (int64_t)p.tokens * p.topk;
+  const dim3 block(kTileThreads<8>);
+  // Up to 20M values the second kernel costs more than reading twice (768 rows x
+  // 7168 of 128 tokens: a call in 8.6 us, and 13.2 with it; 4608 x 4096: 20.2 and
+  // 24.8; 4608 x 7168: 42.9 and 39.1).
+  if ((int64_t)p.m_total * p.cols <= (int64_t)20 << 20) {
+    const dim3 grid((unsigned)(tiles + (entries + 3) / 4));
+    hipLaunchKernelGGL(combine_bwd_kernel<true>, grid, block, 0, stream, p);
+    return hipGetLastError();
+  }
+  if (tiles > 0) hipLaunchKernelGGL(combine_bwd_kernel<false>, dim3(tiles), block, 0, stream, p);
   const int64_t by_entry = (entries + 255) / 256, by_row = (p.m_total + 63) / 64;
   hipLaunchKernelGGL(combine_dweights_kernel, dim3((unsigned)(by_entry > by_row ? by_entry : by_row)), dim3(256), 0, stream, p);
   return hipGetLastError();

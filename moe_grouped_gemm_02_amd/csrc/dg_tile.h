@@ -171,7 +171,7 @@ __device__ __forceinline__ TileUse tile_use(const int32_t* index) {
   return {__ballot(a >= 0), __ballot(b >= 0)};
 }
 
-// Tile of a workgroup in a grid of row_tiles x column_tiles workgroups.  Those
+// Tile of a workgroup, one of the first row_tiles x column_tiles.  Those
 // that run one after another on one XCD (every eighth) take a contiguous eighth
 // of the tiles, row tiles fastest: they write neighbouring pieces of the same
 // columns through one L2 (requantising 32768 x 7168: 92 us against 98 in plain
@@ -179,8 +179,8 @@ __device__ __forceinline__ TileUse tile_use(const int32_t* index) {
 struct TileAt {
   int row, col;
 };
-__device__ __forceinline__ TileAt tile_of_workgroup(int row_tiles) {
-  const int all = gridDim.x, per = all / 8;
+__device__ __forceinline__ TileAt tile_of_workgroup(int row_tiles, int column_tiles) {
+  const int per = row_tiles * column_tiles / 8;
   int b = blockIdx.x;
   if (b < per * 8) b = (b % 8) * per + b / 8;
   return {b % row_tiles, b / row_tiles};

@@ -228,6 +228,12 @@ def test_combine_bwd(transposed, tokens, topk, experts, first, groups, cols, m_t
         check_transposed(host(dqt), host(dsft), ref, live, cols)
 
 
+@pytest.mark.parametrize("transposed", [True, False])
+def test_combine_bwd_tall(transposed):
+    """A layout above the size up to which the weights' gradient is summed apart from the tiles."""
+    test_combine_bwd(transposed, 13000, 3, 4, 1, 3, 512, 41088)
+
+
 def check_transposed(qt, sft, v, live, cols):
     blocks = live.reshape(-1, 128).any(1)
     rows = np.repeat(blocks, 128)
