@@ -32,7 +32,7 @@
  *
  * 1x128 codes of float32 values (the gated unit's output and all gradients):
  *   s = amax / 448 in fp32, at least 2^-126, 0 for an all-zero tile;
- *   q = e4m3( v * (1 / s) ) in fp32.
+ *   q = e4m3( v / s ), the quotient within 2 ulp of fp32.
  * Codes of bf16 values (dispatch, the checkpoint) follow dg_quant_1x128 bit
  * for bit.  No value is rounded to bf16 on the way to its code.
  */

@@ -17,8 +17,8 @@ constexpr int kRowWaves = 4;
 // row 4 y + its wave and every 4 gridDim.y rows on, up to the group's last row in
 // use.  One read of h serves both the unit's output and the checkpoint, and
 // nothing but codes and scales is written.  Bound by memory: 32768 rows x 2048
-// read 0.26 GB and write 0.20 in 89 us (5.2 TB/s).  STREAMING: results larger than
-// the L2s (89 us against 92 with plain stores).
+// read 0.26 GB and write 0.20 in 79 us (5.8 TB/s).  STREAMING: results larger than
+// the L2s (79 us against 81.7 with plain stores).
 template <bool POW2, bool CKPT, bool STREAMING>
 __global__ __launch_bounds__(64 * kRowWaves) void swiglu_kernel(SwigluParams p) {
   const int tiles = p.inter / kBlockK;
@@ -173,15 +173,15 @@ __global__ __launch_bounds__(kTileThreads<4>, 2) void swiglu_bwd_kernel(SwigluBw
     if (t < end) load_raw(p, {t % row_tiles, t / row_tiles}, raw);
     const int64_t row0 = (int64_t)tile.row * kBlockK, ld = 2 * (int64_t)p.inter;
     const int col0 = tile.col * kBlockK;
-    tile_rows<4>(out[0], p.dq + row0 * ld + col0, ld, p.dsf + tile.col * p.ld_dsf + row0, live);
-    tile_rows<4>(out[1], p.dq + row0 * ld + p.inter + col0, ld, p.dsf + (tiles + tile.col) * p.ld_dsf + row0, live);
+    tile_rows<false>(out[0], p.dq + row0 * ld + col0, ld, p.dsf + tile.col * p.ld_dsf + row0, live);
+    tile_rows<false>(out[1], p.dq + row0 * ld + p.inter + col0, ld, p.dsf + (tiles + tile.col) * p.ld_dsf + row0, live);
     uint8_t* dqt = p.dqt + (int64_t)col0 * p.m_total + row0;
     float* dsft = p.dsft + (int64_t)tile.row * p.ld_dsft + col0;
     const ColumnsTo to[3] = {
         {dqt, p.m_total, dsft},
         {dqt + (int64_t)p.inter * p.m_total, p.m_total, dsft + p.inter},
         {p.aqt ? p.aqt + (int64_t)col0 * p.m_total + row0 : nullptr, p.m_total, p.asft + (int64_t)tile.row * p.ld_asft + col0}};
-    tile_columns(out, lds, to);
+    tile_columns<false>(out, lds, to);
   }
 }
 
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kTileThreads<8>) void requant_t_kernel(RequantParam
     for (int c = 0; c < 8; ++c) v[i][c] *= scale;
   }
   const ColumnsTo to[1] = {{p.qt + (int64_t)col0 * p.rows + row0, p.rows, p.sft + (int64_t)tile.row * p.ld_sft + col0}};
-  tile_columns(vs, lds, to);
+  tile_columns<true>(vs, lds, to);
 }
 
 }  // namespace

@@ -341,10 +341,10 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
     }
   }
   if (!APART && i16 < 8 && ((live >> i16) & 1)) p.dots[tile.col * (int64_t)p.m_total + row0 + r0 + i16] = mine;
-  tile_rows<8>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + tile.col * p.ld_dsf + row0, live);
+  tile_rows<true>(v, p.dq + row0 * p.cols + col0, p.cols, p.dsf + tile.col * p.ld_dsf + row0, live);
   if (!p.dqt) return;
   const ColumnsTo to[1] = {{p.dqt + (int64_t)col0 * p.m_total + row0, p.m_total, p.dsft + (int64_t)tile.row * p.ld_dsft + col0}};
-  tile_columns(vs, lds, to);
+  tile_columns<true>(vs, lds, to);
 }
 
 // Workgroup x: the dot products of rows [64 x, 64 x + 64), each wave every fourth

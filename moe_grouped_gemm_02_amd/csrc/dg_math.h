@@ -53,9 +53,10 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 // Stores of results larger than the L2s, which nothing reads back through them:
-// marked as streaming they leave the cached inputs alone (dispatch of 32768 x
-// 7168 rows 124 us, against 133 with plain stores; requantised transpose 84 and
-// 92, combine gradient 243 and 257).
+// marked as streaming they leave the cached inputs alone (calls of 32768 x 7168:
+// plan and dispatch 117 us, against 128 with plain stores; requantised transpose
+// 83.6 and 91.5, combine gradient 252 and 274; gated unit of 32768 x 2048 79 and
+// 81.7).
 __device__ __forceinline__ void store_streaming(void* p, uint4 v) {
   __builtin_nontemporal_store(v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}, static_cast<v4i*>(p));
 }
@@ -69,8 +70,9 @@ __device__ __forceinline__ void store(void* p, uint4 v) {
   if constexpr (STREAMING) store_streaming(p, v);
   else *static_cast<uint4*>(p) = v;
 }
-// Loads of values that are used once (combine of 32768 rows: 95 us, against 107
-// with plain loads).
+// Loads of values that are used once (combine of 32110 rows x 7168: 95 us, against
+// 107.7 with plain loads; requantised transpose 83.6 and 86.5, gated unit's
+// backward 151 and 158).
 __device__ __forceinline__ uint4 load_streaming4(const void* p) {
   const v4i v = __builtin_nontemporal_load(static_cast<const v4i*>(p));
   return make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
