@@ -6,6 +6,13 @@
 
 namespace dg {
 
+// e4m3_x4 without a cleared register to convert into: the two conversions write all
+// four bytes, so whatever a's register holds beside them will do.
+__device__ __forceinline__ uint32_t e4m3_of4(float a, float b, float c, float d) {
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)__float_as_uint(a), false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
 // Scale and its inverse for float32 values: s = amax / 448 (a product with one
 // correction by its residual), kept normal (at least 2^-126) so that its
 // reciprocal is finite; 0 for an all-zero tile.  Scale, inverse and product are
@@ -30,7 +37,7 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
     const float p = v * inv;
     return EXACT ? fmaf(fmaf(-s, p, v), inv, p) : p;
   };
-  return e4m3_x4(q(a), q(b), q(c), q(d));
+  return e4m3_of4(q(a), q(b), q(c), q(d));
 }
 
 // UE8M0 exponent of ue8m0_exponent() for any float32 amax, from its bits:
@@ -88,8 +95,8 @@ __device__ __forceinline__ float amax16(const Values& at) {
 
 template <typename Values>
 __device__ __forceinline__ uint4 encode16(const Values& at) {
-  return make_uint4(e4m3_x4(at(0), at(1), at(2), at(3)), e4m3_x4(at(4), at(5), at(6), at(7)),
-                    e4m3_x4(at(8), at(9), at(10), at(11)), e4m3_x4(at(12), at(13), at(14), at(15)));
+  return make_uint4(e4m3_of4(at(0), at(1), at(2), at(3)), e4m3_of4(at(4), at(5), at(6), at(7)),
+                    e4m3_of4(at(8), at(9), at(10), at(11)), e4m3_of4(at(12), at(13), at(14), at(15)));
 }
 
 // Codes and scale of a bf16 tile, those of the plain activation quantiser bit
