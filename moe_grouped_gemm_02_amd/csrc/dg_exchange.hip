@@ -432,8 +432,10 @@ hipError_t launch_combine_bwd(const CombineBwdParams& p, hipStream_t stream) {
   const dim3 block(kTileThreads<8>);
   // Up to 20M values the second kernel costs more than reading twice (768 rows x
   // 7168 of 128 tokens: a call in 8.6 us, and 13.2 with it; 4608 x 4096: 20.2 and
-  // 24.8; 4608 x 7168: 42.9 and 39.1).
-  if ((int64_t)p.m_total * p.cols <= (int64_t)20 << 20) {
+  // 24.8; 4608 x 7168: 42.9 and 39.1), and up to 32768 entries the waves for those
+  // without a row cost less too (1 of 16 with a row, x 2048: 11.5 and 13.8; of
+  // 131072 entries, x 512: 21.0 and 12.6).
+  if (entries <= 32768 && (int64_t)p.m_total * p.cols <= (int64_t)20 << 20) {
     const dim3 grid((unsigned)(tiles + (entries + 3) / 4));
     hipLaunchKernelGGL(combine_bwd_kernel<true>, grid, block, 0, stream, p);
     return hipGetLastError();

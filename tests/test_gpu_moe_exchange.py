@@ -234,6 +234,11 @@ def test_combine_bwd_tall(transposed):
     test_combine_bwd(transposed, 13000, 3, 4, 1, 3, 512, 41088)
 
 
+def test_combine_bwd_many_entries():
+    """More entries than are summed apart from the tiles, most of them without a row."""
+    test_combine_bwd(True, 8300, 4, 64, 3, 2, 256, 1536)
+
+
 def check_transposed(qt, sft, v, live, cols):
     blocks = live.reshape(-1, 128).any(1)
     rows = np.repeat(blocks, 128)
