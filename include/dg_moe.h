@@ -89,12 +89,14 @@ int dg_moe_route_bf16(const uint16_t* logits, const float* bias, int32_t* ids, f
 /*
  * Gradient of the routing weights with respect to the logits; the choice of
  * experts (and with it the bias and the groups) is held fixed.  With S the
- * sum of the chosen scores (the scores are computed again from the logits):
- *   g_j  = scale * (dw_j - sum_i dw_i s_i / S) / S   (renormalize, S > 0), or
- *          scale * dw_j;
- *   dx_e = s_e (1 - s_e) g_e                          (sigmoid), or
- *          s_e (g_e - sum_i s_i g_i)                  (softmax),
- * with g_e = 0 for experts that were not chosen.  Slots whose id is not in
+ * sum of the chosen scores (the scores are computed again from the logits)
+ * and r_j = s_j / S (0 where S is 0), for the chosen experts:
+ *   z_j  = scale * r_j (dw_j - sum_i dw_i r_i)        (renormalize), or
+ *          scale * s_j dw_j;
+ *   dx_e = z_e (1 - s_e)                              (sigmoid), or
+ *          z_e                                        (softmax, renormalize), or
+ *          z_e - s_e sum_i z_i                        (softmax),
+ * with z_e = 0 for experts that were not chosen.  Slots whose id is not in
  * [0, experts) take no part.  A token's ids must be distinct.
  *   dweights [tokens][topk] float32
  *   dlogits  [tokens][ld_dlogits], of the logits' type; all `experts` columns

@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   float* mine = lds[wave] + lane * V;
   int id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
   if (id >= p.experts) id = -1;
-  float g = id >= 0 ? p.scale * p.dweights[t * p.topk + lane] : 0.0f;
+  const float dw = id >= 0 ? p.dweights[t * p.topk + lane] : 0.0f;
   float x[V], s[V], sel = 0.0f;
   if constexpr (SIGMOID) {
     if (id >= 0) sel = score_sigmoid(widen(row[id]));
@@ -256,22 +256,28 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
     wave_fence();
     if (id >= 0) sel = lds[wave][id];
   }
+  // g: the scores' gradient, or, renormalised, that of the scores' logarithms:
+  // s / S comes first, since the chosen scores' sum S may be so small that a
+  // quotient by it leaves float32.
+  float g = p.scale * dw;
   if (p.renormalize) {
     const float total = wave_sum(sel);
-    if (total != 0.0f) g = (g - wave_sum(g * sel) / total) / total;
-    if (id < 0) g = 0.0f;
+    const float r = total != 0.0f ? sel / total : 0.0f;
+    g = p.scale * r * (dw - wave_sum(dw * r));
   }
   wave_fence();
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[i] = 0.0f;
   wave_fence();
-  if (id >= 0) lds[wave][id] = SIGMOID ? g * sel * (1.0f - sel) : g;
+  if (id >= 0) lds[wave][id] = !SIGMOID ? g : (p.renormalize ? g : g * sel) * (1.0f - sel);
   wave_fence();
-  const float mean = SIGMOID ? 0.0f : wave_sum(g * sel);
+  // Renormalised softmax weights depend on the chosen logits alone: 0 at the others.
+  const bool chosen_alone = SIGMOID || p.renormalize;
+  const float mean = chosen_alone ? 0.0f : wave_sum(g * sel);
   T* to = static_cast<T*>(p.dlogits) + t * p.ld_d;
   float out[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = SIGMOID ? mine[i] : s[i] * (mine[i] - mean);
+  for (int i = 0; i < V; ++i) out[i] = chosen_alone ? mine[i] : s[i] * (mine[i] - mean);
   if constexpr (VEC) {
     Pack<T, V> pack;
 #pragma unroll

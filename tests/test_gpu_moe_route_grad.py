@@ -1,0 +1,87 @@
+"""GPU routing gradient (dg_moe_route_bwd*) where float32 has little room:
+chosen scores whose sum is tiny.
+
+Bounds.  A score carries 2^-18 of its value (float32 exponents of up to 104 in
+magnitude carry 2^-19, the sum, the quotient and the reciprocal a few 2^-23)
+and, below the normal range, 2^-149; a weight r = s / S of k chosen experts
+therefore 2^-17 of its value and (k + 1) 2^-149 / S, and both enter the gradient
+r (dw - sum dw r) twice.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def _bwd(dg, x, ids, dw, bf16=False, **kw):
+    dt = torch.bfloat16 if bf16 else torch.float32
+    logits = torch.as_tensor(x, device="cuda").to(dt)
+    dx = torch.full_like(logits, float("nan"))
+    (dg.dg_moe_route_bwd_bf16 if bf16 else dg.dg_moe_route_bwd)(
+        logits, torch.as_tensor(ids, dtype=torch.int32, device="cuda"), torch.as_tensor(dw, device="cuda"), dx, **kw)
+    return dx.float().cpu().numpy().astype(np.float64)
+
+
+def _weight_bound(x, ids, dw, score, scale):
+    """Error of scale * r (dw - sum dw r) at the chosen experts, scattered over the row."""
+    s = np.take_along_axis(moe.scores(x, score), ids, 1)
+    total = s.sum(1, keepdims=True)
+    most = np.abs(dw).max(1, keepdims=True)
+    part = 4 * scale * most * (2.0 ** -17 * s / total + (ids.shape[1] + 1) ** 2 * 2.0 ** -149 / total) + 1e-30
+    full = np.zeros(x.shape)
+    np.put_along_axis(full, ids, part, 1)
+    return full
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("experts,topk", [(4, 4), (64, 8), (72, 6), (256, 8), (1000, 32)])
+@pytest.mark.parametrize("low,high", [(-91.0, -88.0), (-97.0, -88.0), (-60.0, -50.0)])
+def test_tiny_sigmoids(low, high, experts, topk, bf16):
+    """All experts far below zero: the chosen sigmoids' sum is near or below the
+    smallest normal number, the renormalised weights and their gradient are not."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts + topk)
+    x = rng.uniform(low, high, (33, experts)).astype(np.float32)
+    x = torch.as_tensor(x).bfloat16().float().numpy() if bf16 else x
+    ids, _ = moe.route(x, topk, "sigmoid")
+    dw = rng.standard_normal(ids.shape).astype(np.float32)
+    got = _bwd(dg, x, ids, dw, bf16, score="sigmoid", scale=2.5)
+    ref = moe.route_bwd(x, ids, dw, "sigmoid", True, 2.5)
+    assert np.all(np.abs(got - ref) <= _weight_bound(x, ids, dw, "sigmoid", 2.5) + (2.0 ** -8 * np.abs(ref) if bf16 else 0))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("experts,topk", [(5, 3), (64, 8), (72, 6), (256, 8), (1000, 32)])
+@pytest.mark.parametrize("below", [5.0, 60.0, 92.0])
+def test_softmax_of_tiny_chosen_scores(below, experts, topk, bf16):
+    """One expert far above the chosen ones, as a selection bias makes it: the
+    gradient stays with the chosen experts and is exactly zero at the others."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts * 3 + topk)
+    x = rng.uniform(-2.0, 2.0, (33, experts)).astype(np.float32) - np.float32(below)
+    x[:, 1] = 0.0
+    x = torch.as_tensor(x).bfloat16().float().numpy() if bf16 else x
+    ids = np.stack([rng.permutation(np.delete(np.arange(experts), 1))[:topk] for _ in range(len(x))])
+    dw = rng.standard_normal(ids.shape).astype(np.float32)
+    got = _bwd(dg, x, ids, dw, bf16, score="softmax", scale=2.5)
+    ref = moe.route_bwd(x, ids, dw, "softmax", True, 2.5)
+    chosen = np.zeros(x.shape, dtype=bool)
+    np.put_along_axis(chosen, ids, True, 1)
+    assert np.all(got[~chosen] == 0)
+    bound = _weight_bound(x, ids, dw, "softmax", 2.5) + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+    assert np.all(np.abs(got - ref)[chosen] <= bound[chosen])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_that_underflow_have_no_gradient(score):
+    dg = require_gpu()
+    x = np.full((3, 64), -2000.0, dtype=np.float32)
+    x[:, 9] = 0.0
+    ids = np.array([[3, 4], [5, -1], [63, 0]])
+    got = _bwd(dg, x, ids, np.ones((3, 2), dtype=np.float32), score=score)
+    assert np.all(got == 0)
