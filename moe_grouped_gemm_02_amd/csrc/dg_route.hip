@@ -71,6 +71,15 @@ __device__ __forceinline__ float score_sigmoid(float x) {
   return e * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// s = 1 / (1 + e^-x) and 1 - s, each with its own relative accuracy: the smaller
+// one is e^-|x| times the larger, not a difference from 1.
+__device__ __forceinline__ void both_sigmoids(float x, float& s, float& rest) {
+  const float e = exp_to_80(-fabsf(x));
+  const float large = reciprocal(1.0f + e), small = e * large;
+  s = x < 0.0f ? small : large;
+  rest = x < 0.0f ? large : small;
+}
+
 // Scores of the wave's token.
 template <int V>
 __device__ __forceinline__ void scores(const float (&x)[V], float (&s)[V], bool sigmoid_scores) {
@@ -245,9 +254,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   int id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
   if (id >= p.experts) id = -1;
   const float dw = id >= 0 ? p.dweights[t * p.topk + lane] : 0.0f;
-  float x[V], s[V], sel = 0.0f;
+  float x[V], s[V], sel = 0.0f, rest = 0.0f;
   if constexpr (SIGMOID) {
-    if (id >= 0) sel = score_sigmoid(widen(row[id]));
+    if (id >= 0) both_sigmoids(widen(row[id]), sel, rest);
   } else {
     load_row<VEC>(row, p.experts, lane, lds[wave], x);
     scores<V>(x, s, false);
@@ -269,7 +278,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) mine[i] = 0.0f;
   wave_fence();
-  if (id >= 0) lds[wave][id] = !SIGMOID ? g : (p.renormalize ? g : g * sel) * (1.0f - sel);
+  if (id >= 0) lds[wave][id] = !SIGMOID ? g : (p.renormalize ? g : g * sel) * rest;
   wave_fence();
   // Renormalised softmax weights depend on the chosen logits alone: 0 at the others.
   const bool chosen_alone = SIGMOID || p.renormalize;

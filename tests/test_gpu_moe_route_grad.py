@@ -85,3 +85,43 @@ def test_scores_that_underflow_have_no_gradient(score):
     ids = np.array([[3, 4], [5, -1], [63, 0]])
     got = _bwd(dg, x, ids, np.ones((3, 2), dtype=np.float32), score=score)
     assert np.all(got == 0)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts,topk", [(1, 1), (5, 3), (64, 8), (72, 6), (256, 8), (1000, 32)])
+def test_slope_of_saturated_sigmoids(experts, topk, renormalize, bf16):
+    """Logits up to 40 of both signs: s (1 - s) keeps its relative accuracy where
+    1 - s is far below one unit in the last place of s.  Exponents of up to 58 in
+    magnitude carry 2^-19, the rest a few 2^-23."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts * 7 + topk)
+    x = rng.uniform(-40.0, 40.0, (65, experts)).astype(np.float32)
+    x[::3] = np.abs(x[::3])
+    x = torch.as_tensor(x).bfloat16().float().numpy() if bf16 else x
+    ids = np.stack([rng.permutation(experts)[:topk] for _ in range(len(x))])
+    dw = rng.standard_normal(ids.shape).astype(np.float32)
+    got = np.take_along_axis(_bwd(dg, x, ids, dw, bf16, score="sigmoid", renormalize=renormalize, scale=2.5), ids, 1)
+    ref = np.take_along_axis(moe.route_bwd(x, ids, dw, "sigmoid", False, 1.0), ids, 1)  # dw s (1 - s)
+    s = np.take_along_axis(moe.scores(x, "sigmoid"), ids, 1)
+    rest = np.take_along_axis(moe.scores(-x, "sigmoid"), ids, 1)
+    if renormalize:
+        r = s / s.sum(1, keepdims=True)
+        ref = 2.5 * r * (dw - (dw * r).sum(1, keepdims=True)) * rest
+        bound = 2.0 ** -17 * 2.5 * r * rest * (np.abs(dw) + (np.abs(dw) * r).sum(1, keepdims=True))
+    else:
+        ref = 2.5 * dw * s * rest
+        bound = 2.0 ** -18 * np.abs(ref)
+    assert np.all(np.abs(got - ref) <= bound + (2.0 ** -8 * np.abs(ref) if bf16 else 0) + 1e-37)
+
+
+def test_slope_past_the_range_of_the_exponent():
+    """Logits of 60 to 3e38: 1 - s goes down to float32's smallest numbers and to 0, never below."""
+    dg = require_gpu()
+    x = np.array([[60.0, 80.0, 85.0, 88.0, 95.0, 200.0, 3e38, np.inf], [-60.0, -80.0, -85.0, -88.0, -95.0, -200.0, -3e38, -np.inf]],
+                 dtype=np.float32)
+    ids = np.tile(np.arange(8), (2, 1))
+    got = _bwd(dg, x, ids, np.ones((2, 8), dtype=np.float32), score="sigmoid", renormalize=False)
+    e = np.exp(-np.abs(x.astype(np.float64)))
+    ref = e / (1.0 + e) ** 2
+    assert np.all(got >= 0) and np.all(np.abs(got - ref) <= 2.0 ** -17 * ref + 2.0 ** -147)
