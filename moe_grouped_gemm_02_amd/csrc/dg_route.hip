@@ -74,7 +74,7 @@ __device__ __forceinline__ float score_sigmoid(float x) {
 // s = 1 / (1 + e^-x) and 1 - s, each with its own relative accuracy: the smaller
 // one is e^-|x| times the larger, not a difference from 1.
 __device__ __forceinline__ void both_sigmoids(float x, float& s, float& rest) {
-  const float e = exp_to_80(-fabsf(x));
+  const float e = x == x ? exp_to_80(-fabsf(x)) : x;
   const float large = reciprocal(1.0f + e), small = e * large;
   s = x < 0.0f ? small : large;
   rest = x < 0.0f ? large : small;

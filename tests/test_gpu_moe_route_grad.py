@@ -125,3 +125,18 @@ def test_slope_past_the_range_of_the_exponent():
     e = np.exp(-np.abs(x.astype(np.float64)))
     ref = e / (1.0 + e) ** 2
     assert np.all(got >= 0) and np.all(np.abs(got - ref) <= 2.0 ** -17 * ref + 2.0 ** -147)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_nan_logit_of_a_given_expert_shows(renormalize):
+    """ids that name an expert whose logit is NaN: its own score is NaN, and with it
+    all of the token's renormalised weights; other tokens keep their gradient."""
+    dg = require_gpu()
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((3, 16)).astype(np.float32)
+    x[1, 5] = np.nan
+    ids = np.array([[5, 2, 9]] * 3)
+    got = _bwd(dg, x, ids, np.tile(np.float32([1, 2, 3]), (3, 1)), score="sigmoid", renormalize=renormalize)
+    want = np.zeros((3, 16), dtype=bool)
+    want[1, [5, 2, 9] if renormalize else [5]] = True
+    assert np.array_equal(np.isnan(got), want)
