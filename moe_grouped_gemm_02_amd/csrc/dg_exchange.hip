@@ -14,7 +14,9 @@ namespace {
 // A stable counting sort.  Blocks of 1024 entries count their experts (one
 // launch) and place their entries (another): the rank of an entry is the count
 // of its expert in the blocks before, in the waves before, and in the lanes
-// before, which a ballot for each bit of the expert's number tells.  Up to 4096
+// before, which a ballot for each bit of the expert's number tells.  The counts of
+// the blocks before are added up by each block, or, where there are many, by a
+// launch in between.  Up to 4096
 // entries one workgroup does it all in one launch (1024 entries of 32 experts:
 // 4.7 us, against 1.3 + 4.7 in two launches).  Both are a chain of reads and
 // barriers, not a stream: 131072 entries of 4 experts take 3.0 + 4.8 us for 2 MB.
@@ -58,10 +60,55 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanParams p) 
   if (tid < p.groups) p.hist[(int64_t)blockIdx.x * p.groups + tid] = count[tid];
 }
 
+// Replaces each block's counts by their sums over the blocks before and puts the
+// groups' totals behind the last block's.  Workgroup: 2^shift groups, whose
+// columns of counts are cut into as many parts as there are threads for.
+constexpr int kScanShift = 4;
+
+__global__ __launch_bounds__(kPlanThreads) void plan_scan_kernel(PlanParams p, int shift) {
+  __shared__ int sums[kPlanThreads];
+  const int tid = threadIdx.x, part = tid >> shift, parts = kPlanThreads >> shift;
+  const int col = (blockIdx.x << shift) + (tid & ((1 << shift) - 1));
+  const int per = (p.blocks + parts - 1) / parts;
+  const int lo = min(part * per, p.blocks), hi = min(lo + per, p.blocks);
+  const bool in = col < p.groups;
+  int32_t* const hist = p.hist + (in ? col : 0);
+  // Eight counts at a time, so that their reads are in flight together.
+  auto read8 = [&](int b, int (&c)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) c[u] = in && b + u < hi ? hist[(int64_t)(b + u) * p.groups] : 0;
+  };
+  int sum = 0, c[8];
+  for (int b = lo; b < hi; b += 8) {
+    read8(b, c);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum += c[u];
+  }
+  sums[tid] = sum;
+  __syncthreads();
+  for (int off = 1 << shift; off < kPlanThreads; off <<= 1) {
+    const int other = tid >= off ? sums[tid - off] : 0;
+    __syncthreads();
+    sums[tid] += other;
+    __syncthreads();
+  }
+  int before = sums[tid] - sum;
+  if (!in) return;
+  for (int b = lo; b < hi; b += 8) {
+    read8(b, c);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (b + u < hi) hist[(int64_t)(b + u) * p.groups] = before;
+      before += c[u];
+    }
+  }
+  if (part == parts - 1) hist[(int64_t)p.blocks * p.groups] = before;
+}
+
 // Places the entries and fills the index arrays of the layout's rows.  ONE: one
 // workgroup, which counts the entries itself; otherwise block b places entries
-// [1024 b, 1024 b + 1024) with the counts of all blocks (blocks past the last
-// entry help with the rows alone).
+// [1024 b, 1024 b + 1024) with the counts of all blocks or their sums (blocks past
+// the last entry help with the rows alone).
 template <bool ONE>
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) {
   __shared__ int start[kMaxLocalExperts + 1];  // first row of each group
@@ -81,18 +128,25 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
       if (e >= 0) atomicAdd(&count[e], 1);
     }
   } else {
-    const int before = blockIdx.x * p.groups, all = p.blocks * p.groups;
-    for (int i = tid; i < all; i += kPlanThreads) {
-      const int v = p.hist[i], e = i % p.groups;
-      atomicAdd(&count[e], v);
-      if (i < before) atomicAdd(&base[e], v);
+    if (p.scanned) {
+      if (tid < p.groups) {
+        count[tid] = p.hist[(int64_t)p.blocks * p.groups + tid];
+        if (blockIdx.x < p.blocks) base[tid] = p.hist[(int64_t)blockIdx.x * p.groups + tid];
+      }
+    } else {
+      const int before = blockIdx.x * p.groups, all = p.blocks * p.groups;
+      for (int i = tid; i < all; i += kPlanThreads) {
+        const int v = p.hist[i], e = i % p.groups;
+        atomicAdd(&count[e], v);
+        if (i < before) atomicAdd(&base[e], v);
+      }
     }
   }
   __syncthreads();
   // Starts of the groups: exclusive sums of their sizes.
   {
     uint32_t size = 0;
-    if (tid < p.groups) size = p.masked ? p.m_max : (uint32_t)(count[tid] + kBlockK - 1) / kBlockK * kBlockK;
+    if (tid < p.groups) size = p.masked ? p.m_max : ((uint32_t)count[tid] + kBlockK - 1) / kBlockK * kBlockK;
     uint32_t sum = size;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -377,7 +431,7 @@ __global__ __launch_bounds__(256) void combine_dweights_kernel(CombineBwdParams 
 }  // namespace
 
 size_t plan_workspace_bytes(int64_t entries, int groups) {
-  return (size_t)plan_blocks(entries) * groups * sizeof(int32_t);
+  return ((size_t)plan_blocks(entries) + 1) * groups * sizeof(int32_t);
 }
 
 hipError_t launch_plan(const PlanParams& params, hipStream_t stream) {
@@ -389,7 +443,18 @@ hipError_t launch_plan(const PlanParams& params, hipStream_t stream) {
   } else {
     const int for_rows = (int)(((int64_t)p.layout_rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
     const int most = for_rows < 256 ? for_rows : 256;
+    // Few counts are added up by every block again, many by a launch of their own,
+    // which costs 2 to 3 us (131072 entries of 4 groups: 9.6 us against 11.9; of 128:
+    // 14.3 and 14.0, of 1024: 49.5 and 18.0; 1M of 4: 19.4 both, of 256: 159 and 30.3)
+    // and keeps the work in proportion to the entries.
+    p.scanned = (int64_t)p.blocks * (p.groups > 16 ? p.groups : 16) >= 16384;
     hipLaunchKernelGGL(plan_count_kernel, dim3(p.blocks), block, 0, stream, p);
+    if (p.scanned) {
+      int shift = 0;
+      while (shift < kScanShift && 1 << shift < p.groups) ++shift;
+      const int columns = (p.groups + (1 << shift) - 1) >> shift;
+      hipLaunchKernelGGL(plan_scan_kernel, dim3(columns), block, 0, stream, p, shift);
+    }
     hipLaunchKernelGGL(plan_place_kernel<false>, dim3(p.blocks > most ? p.blocks : most), block, 0, stream, p);
   }
   return hipGetLastError();

@@ -54,8 +54,9 @@ struct PlanParams {
   int32_t* m_indices;  // contiguous only
   int32_t* k_offsets;  // contiguous only
   int32_t* masked_m;   // masked only
-  int32_t* hist;       // [blocks][groups] counts
+  int32_t* hist;       // [blocks + 1][groups] counts
   int blocks;          // of 1024 entries (set by the launch)
+  int scanned;         // whether hist holds sums over the blocks before (set by the launch)
   int entries;         // tokens * topk
   int first, groups;
   int masked, m_max;   // masked layout and its rows per group
