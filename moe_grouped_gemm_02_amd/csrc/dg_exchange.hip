@@ -276,14 +276,15 @@ __global__ __launch_bounds__(64 * kRowWaves) void dispatch_kernel(DispatchParams
 
 // ---------------------------------------------------------------- combine --
 
-// Workgroup (t, y): 2048 columns of token t, 8 a thread: one pass over the rows,
-// sums in float32 registers, the only rounding at the end.  Bound by the reads:
-// 32110 rows x 7168 into 4096 tokens in 95 us, 0.46 GB read and 0.06 written
-// (5.5 TB/s).
+// Workgroup (x, y, z): 2048 columns, 8 a thread, of token x (past those of a smaller
+// z): one pass over the rows, sums in float32 registers, the only rounding at the
+// end.  Bound by the reads: 32110 rows x 7168 into 4096 tokens in 95 us, 0.46 GB
+// read and 0.06 written (5.5 TB/s).
 constexpr int kCombineThreads = 256;
 
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineParams p) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
+  if (t >= p.tokens) return;
   const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
   if (col >= p.cols) return;
   float acc[8];
@@ -486,7 +487,8 @@ hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t strea
 }
 
 hipError_t launch_combine(const CombineParams& p, hipStream_t stream) {
-  const dim3 grid(p.tokens, (p.cols / 8 + kCombineThreads - 1) / kCombineThreads);
+  const GridXY by_token = spread(p.tokens);
+  const dim3 grid(by_token.x, (p.cols / 8 + kCombineThreads - 1) / kCombineThreads, by_token.y);
   hipLaunchKernelGGL(combine_kernel, grid, dim3(kCombineThreads), 0, stream, p);
   return hipGetLastError();
 }

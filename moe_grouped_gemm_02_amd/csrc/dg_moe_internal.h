@@ -27,6 +27,17 @@ inline Divisor divisor(uint32_t d) {
   return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l - 1};
 }
 
+// A launch of 2^32 threads or more along one dimension of its grid is not made, or
+// loses those past 2^32 without an error: workgroups of up to 256 threads that are
+// counted by tokens are spread over two dimensions, x first.
+struct GridXY {
+  unsigned x, y;
+};
+inline GridXY spread(int64_t workgroups) {
+  constexpr int64_t kMost = (int64_t)1 << 23;
+  return workgroups <= kMost ? GridXY{(unsigned)workgroups, 1u} : GridXY{(unsigned)kMost, (unsigned)((workgroups + kMost - 1) / kMost)};
+}
+
 struct RouteParams {
   const void* logits;  // [tokens][ld], fp32 or bf16
   const float* bias;   // null: none

@@ -119,7 +119,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteParams p) {
   __shared__ float lds[kWaves][64 * V];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
   if (t >= p.tokens) return;
   float x[V], s[V], bias[V];
   uint32_t key[V];  // 0: cannot be chosen
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
   __shared__ float lds[kWaves][64 * V];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
   if (t >= p.tokens) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
   float* mine = lds[wave] + lane * V;
@@ -307,7 +307,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteParams p) {
 
 template <bool VEC, typename T, int V>
 void go(const RouteParams& p, bool bwd, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)p.tokens + kWaves - 1) / kWaves)), block(64 * kWaves);
+  const GridXY by_token = spread(((int64_t)p.tokens + kWaves - 1) / kWaves);
+  const dim3 grid(by_token.x, by_token.y), block(64 * kWaves);
   if (!bwd) {
     if (p.bias && p.groups > 1) hipLaunchKernelGGL((route_kernel<VEC, T, V, true, true>), grid, block, 0, stream, p);
     else if (p.bias) hipLaunchKernelGGL((route_kernel<VEC, T, V, true, false>), grid, block, 0, stream, p);
