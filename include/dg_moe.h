@@ -30,6 +30,9 @@
  * points (as for dg_quant_1x128); in rows that the layout leaves out they are
  * never looked at.
  *
+ * Matrices have at most 65535 * 128 columns (h, hq and what has their width
+ * included), byte offsets stay below 2^46; smaller limits stand with the calls.
+ *
  * 1x128 codes of float32 values (the gated unit's output and all gradients):
  *   s = amax / 448 in fp32, at least 2^-126, 0 for an all-zero tile;
  *   q = e4m3( v / s ), the quotient within 2 ulp of fp32.
@@ -190,7 +193,8 @@ int dg_moe_combine(const uint16_t* d, const int32_t* rows, const float* weights,
  *   dweights [tokens][topk] = sum_n dy[t][n] * d[rows[t][j]][n], 0 without a row
  * workspace: dg_get_moe_combine_bwd_workspace_size(m_total, cols) bytes,
  * 16-byte aligned, contents irrelevant.
- * cols % 128 == 0, m_total % 128 == 0; ld_dy, ld_d multiples of 8;
+ * cols % 128 == 0, m_total % 128 == 0, m_total < 2^30, m_total * cols < 2^38;
+ * ld_dy, ld_d multiples of 8;
  * ld_dsf >= m_total, ld_dsft >= cols, multiples of 4; all pointers but the
  * index arrays', weights' and dweights' 16-byte aligned.
  */
@@ -216,7 +220,7 @@ size_t dg_get_moe_combine_bwd_workspace_size(int m_total, int cols);
  * Rows in use: all (m_indices and masked_m NULL), those with m_indices[r] >= 0
  * (m_indices [rows]; needs num_groups == 1), or the first masked_m[g] of
  * group g (masked_m [num_groups]).  Other rows are not written.
- * inter % 128 == 0; ld_h >= 2 inter, a multiple of 8; ld_sf, ld_hsf >= rows,
+ * inter % 128 == 0, num_groups <= 65535; ld_h >= 2 inter, a multiple of 8; ld_sf, ld_hsf >= rows,
  * multiples of 4; data pointers 16-byte aligned.
  */
 int dg_swiglu_quant(const uint16_t* h, const int32_t* m_indices, const int32_t* masked_m,
@@ -245,8 +249,8 @@ int dg_swiglu_quant_ue8m0(const uint16_t* h, const int32_t* m_indices, const int
  * are not written.
  *   hq [m_total][2 inter] e4m3, hsf [2 inter/128][ld_hsf] fp32
  *   dact [m_total][ld_dact] bf16
- * inter % 128 == 0, m_total % 128 == 0; ld_dact >= inter, % 8; ld_hsf and
- * ld_dsf >= m_total, ld_dsft >= 2 inter, ld_asft >= inter, all % 4; data
+ * inter % 128 == 0, m_total % 128 == 0, m_total * inter < 2^45; ld_dact >= inter,
+ * % 8; ld_hsf and ld_dsf >= m_total, ld_dsft >= 2 inter, ld_asft >= inter, all % 4; data
  * pointers 16-byte aligned.
  */
 int dg_swiglu_bwd(const uint8_t* hq, const float* hsf, const uint16_t* dact,
@@ -260,7 +264,8 @@ int dg_swiglu_bwd(const uint8_t* hq, const float* hsf, const uint16_t* dact,
  * column and 128 rows, transposed:
  *   qt [cols][rows] e4m3, sft [rows/128][ld_sft] fp32
  * Rows in use, zeros and unwritten blocks as for dg_swiglu_bwd.
- * rows % 128 == 0, cols % 128 == 0; ld_sf >= rows, ld_sft >= cols, % 4.
+ * rows % 128 == 0, cols % 128 == 0, rows * cols < 2^38; ld_sf >= rows,
+ * ld_sft >= cols, % 4.
  */
 int dg_requant_t(const uint8_t* q, const float* sf, const int32_t* m_indices, uint8_t* qt,
                  float* sft, int rows, int cols, int64_t ld_sf, int64_t ld_sft, void* stream);

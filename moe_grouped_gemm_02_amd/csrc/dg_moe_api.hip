@@ -16,9 +16,10 @@ using dg::fail;
 using dg::ok;
 
 constexpr int64_t kRowLimit = (int64_t)1 << 31;
+constexpr int64_t kWorkgroupLimit = (int64_t)1 << 24;  // of 256 threads in one grid dimension
 // Byte offsets are 64-bit; a matrix this large is a wrong argument.
 constexpr int64_t kByteLimit = (int64_t)1 << 46;
-// Largest grid y dimension, in 128-column tiles.
+// A row wider than this is a wrong argument.
 constexpr int kMaxCols = 65535 * 128;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -58,10 +59,11 @@ int check_layout(int rows, int groups) {
   return DG_SUCCESS;
 }
 
-// Tiles of 128 x 128 that a grid counts with 32 bits.
-int check_tiles(int rows, int cols) {
-  if ((int64_t)(rows / 128) * (cols / 128) >= kRowLimit)
-    return fail(DG_ERR_UNSUPPORTED_SHAPE, "2^31 or more tiles (%d x %d)", rows, cols);
+// Tiles of 128 x 128.  Kernels that walk over them count with 32 bits; those that
+// take a workgroup of 256 threads for each need fewer than 2^32 threads in all.
+int check_tiles(int rows, int cols, bool workgroup_each) {
+  if ((int64_t)(rows / 128) * (cols / 128) >= (workgroup_each ? kWorkgroupLimit : kRowLimit))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "2^%d or more tiles (%d x %d)", workgroup_each ? 24 : 31, rows, cols);
   return DG_SUCCESS;
 }
 
@@ -284,7 +286,9 @@ int dg_moe_combine_bwd(const uint16_t* dy, const uint16_t* d, const int32_t* src
   DG_TRY(check_layout(m_total, 1));
   if (m_total % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m_total=%d is not a multiple of 128", m_total);
   DG_TRY(check_cols("cols", cols, 128));
-  DG_TRY(check_tiles(m_total, cols));
+  DG_TRY(check_tiles(m_total, cols, true));
+  if (m_total / 64 >= kWorkgroupLimit)  // a workgroup for 64 rows sums the weights' gradient
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "m_total=%d is 2^30 or more", m_total);
   if (!dqt != !dsft) return fail(DG_ERR_INVALID_VALUE, "dqt and dsft go together");
   DG_TRY(check_ld("ld_dy", ld_dy, cols, 8, tokens, 2));
   DG_TRY(check_ld("ld_d", ld_d, cols, 8, m_total, 2));
@@ -326,7 +330,7 @@ int dg_swiglu_bwd(const uint8_t* hq, const float* hsf, const uint16_t* dact, con
   if (m_total % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "m_total=%d is not a multiple of 128", m_total);
   DG_TRY(check_cols("inter", inter, 128));
   if (inter > kMaxCols / 2) return fail(DG_ERR_UNSUPPORTED_SHAPE, "inter=%d is larger than %d", inter, kMaxCols / 2);
-  DG_TRY(check_tiles(m_total, inter));
+  DG_TRY(check_tiles(m_total, inter, false));
   if (!aqt != !asft) return fail(DG_ERR_INVALID_VALUE, "aqt and asft go together");
   DG_TRY(check_ld("ld_hsf", ld_hsf, m_total, 4, inter / 64, 4));
   DG_TRY(check_ld("ld_dact", ld_dact, inter, 8, m_total, 2));
@@ -348,7 +352,7 @@ int dg_requant_t(const uint8_t* q, const float* sf, const int32_t* m_indices, ui
   DG_TRY(check_layout(rows, 1));
   if (rows % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "rows=%d is not a multiple of 128", rows);
   DG_TRY(check_cols("cols", cols, 128));
-  DG_TRY(check_tiles(rows, cols));
+  DG_TRY(check_tiles(rows, cols, true));
   DG_TRY(check_ld("ld_sf", ld_sf, rows, 4, cols / 128, 4));
   DG_TRY(check_ld("ld_sft", ld_sft, cols, 4, rows / 128, 4));
   if (rows == 0 || cols == 0) return ok();
