@@ -59,8 +59,12 @@ def _score(score):
 
 
 # Stream handle of a device's current stream: what torch.cuda.current_stream()
-# wraps, without making the wrapper (1.5 us of a call that has 6 us in all).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# wraps, without making the wrapper (1.5 us of a call that has 6 us in all); a
+# torch without that private call has the public one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _stream(t):
