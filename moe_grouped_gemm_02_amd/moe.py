@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import _BF, _I, _L, _P, _S, _U8, _check, _contig, _expect, _lib, _ptr, _row_major, _ws
+from . import _BF, _I, _L, _P, _S, _U8, _check, _contig, _expect, _lib, _row_major
 
 _F = ctypes.c_float
 
@@ -167,6 +167,16 @@ def _scales(t, name, dtypes, lead, rows):
     return t.data_ptr(), t.shape[-1]
 
 
+def _workspace(t):
+    """Address and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _expect(t, "workspace", (getattr(t, "dtype", None),))
+        _contig(t, "workspace")
+    return t.data_ptr(), t.nbytes
+
+
 # ---------------------------------------------------------------- routing --
 
 def _route(fn, dtypes, logits, ids, weights, bias, score, expert_groups, topk_groups, group_top, renormalize, scale):
@@ -265,7 +275,7 @@ def dg_moe_plan_contiguous(ids, rows, src, m_indices, k_offsets, first_expert=0,
     k_offsets_at, ends = _vector(k_offsets, "k_offsets")
     _check("dg_moe_plan_contiguous", _lib.dg_moe_plan_contiguous(
         ids_at, rows_at, src_at, m_indices_at, k_offsets_at, tokens, topk, int(first_expert), ends - 1, m_total,
-        _ptr(workspace), _ws(workspace), _stream(ids)))
+        *_workspace(workspace), _stream(ids)))
     return rows, src, m_indices, k_offsets
 
 
@@ -278,7 +288,7 @@ def dg_moe_plan_masked(ids, rows, src, masked_m, first_expert=0, workspace=None)
         raise ValueError("src must hold the same number of rows for every group")
     _check("dg_moe_plan_masked", _lib.dg_moe_plan_masked(
         ids_at, rows_at, src_at, masked_m_at, tokens, topk, int(first_expert), groups, layout_rows // groups,
-        _ptr(workspace), _ws(workspace), _stream(ids)))
+        *_workspace(workspace), _stream(ids)))
     return rows, src, masked_m
 
 
@@ -369,7 +379,7 @@ def dg_moe_combine_bwd(dy, d, src, rows, weights, dq, dsf, dqt, dsft, dweights, 
         dsft_at, ld_dsft = _scales(dsft, "dsft", _F32, (m_total // 128,), cols)
     _check("dg_moe_combine_bwd", _lib.dg_moe_combine_bwd(
         dy_at, d_at, src_at, rows_at, weights_at, dq_at, dsf_at, dqt_at, dsft_at, dweights_at, tokens, topk, cols,
-        m_total, ld_dy, ld_d, ld_dsf, ld_dsft, _ptr(workspace), _ws(workspace), _stream(dy)))
+        m_total, ld_dy, ld_d, ld_dsf, ld_dsft, *_workspace(workspace), _stream(dy)))
     return dq, dsf, dqt, dsft, dweights
 
 
