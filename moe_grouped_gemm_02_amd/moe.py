@@ -71,6 +71,18 @@ def _stream(t):
     return _raw_stream(t.get_device())
 
 
+# Sizes are 32-bit numbers in the library, and ctypes would drop the bits above.
+_MOST = 2 ** 31 - 1
+
+
+def _int(value, name):
+    if value.__class__ is not int:
+        value = int(value)
+    if -_MOST <= value <= _MOST:
+        return value
+    raise ValueError(f"{name}={value} is 2^31 or more")
+
+
 def _shape(t, name, want):
     if tuple(t.shape) != tuple(want):
         raise ValueError(f"{name} must have shape {tuple(want)}, has {tuple(t.shape)}")
@@ -104,6 +116,8 @@ def _topk(t, name, tokens):
     except (AttributeError, IndexError):
         _expect(t, name, _I32, 2)
         raise
+    if topk > _MOST:
+        raise ValueError(f"{name} has 2^31 or more columns")
     return _dense(t, name, _I32, (tokens, topk)), topk
 
 
@@ -114,12 +128,12 @@ def _matrix(t, name, dtypes):
         if t.is_cuda and t.dtype in dtypes:
             rows, cols = t.shape
             ld, unit = t.stride()
-            if unit == 1 and rows and cols:
+            if unit == 1 and 0 < rows <= _MOST and 0 < cols <= _MOST:
                 return t.data_ptr(), rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
     except (AttributeError, ValueError):
         pass
     _expect(t, name, dtypes, 2)
-    rows, cols = t.shape
+    rows, cols = (_int(n, f"size of {name}") for n in t.shape)
     if rows <= 1 or cols == 0:
         if cols > 1 and rows:
             _row_major(t, name)
@@ -185,8 +199,9 @@ def _route(fn, dtypes, logits, ids, weights, bias, score, expert_groups, topk_gr
     weights_at = _dense(weights, "weights", _F32, (tokens, topk))
     bias_at = _dense_or_none(bias, "bias", _F32, (experts,))
     _check(fn, _FUNCTIONS[fn](
-        logits_at, bias_at, ids_at, weights_at, tokens, experts, topk, ld, _score(score), int(expert_groups),
-        int(topk_groups), int(group_top), bool(renormalize), scale, _stream(logits)))
+        logits_at, bias_at, ids_at, weights_at, tokens, experts, topk, ld, _score(score),
+        _int(expert_groups, "expert_groups"), _int(topk_groups, "topk_groups"), _int(group_top, "group_top"),
+        bool(renormalize), scale, _stream(logits)))
     return ids, weights
 
 
@@ -242,12 +257,13 @@ def _vector(t, name):
     try:
         if t.is_cuda and t.dtype is torch.int32 and t.is_contiguous():
             n, = t.shape
-            return t.data_ptr(), n
+            if n <= _MOST:
+                return t.data_ptr(), n
     except (AttributeError, ValueError):
         pass
     _expect(t, name, _I32, 1)
     _contig(t, name)
-    return t.data_ptr(), t.shape[0]
+    return t.data_ptr(), _int(t.shape[0], f"size of {name}")
 
 
 def _entries(ids, rows):
@@ -257,12 +273,15 @@ def _entries(ids, rows):
     except (AttributeError, ValueError):
         _expect(ids, "ids", _I32, 2)
         raise
+    if tokens > _MOST or topk > _MOST:
+        raise ValueError(f"ids of shape {tuple(ids.shape)} has a size of 2^31 or more")
     shape = tokens, topk
     return _dense(ids, "ids", _I32, shape), _dense(rows, "rows", _I32, shape), tokens, topk
 
 
 def dg_get_moe_plan_workspace_size(tokens, topk, num_groups):
-    return int(_lib.dg_get_moe_plan_workspace_size(int(tokens), int(topk), int(num_groups)))
+    return int(_lib.dg_get_moe_plan_workspace_size(
+        _int(tokens, "tokens"), _int(topk, "topk"), _int(num_groups, "num_groups")))
 
 
 def dg_moe_plan_contiguous(ids, rows, src, m_indices, k_offsets, first_expert=0, workspace=None):
@@ -274,8 +293,8 @@ def dg_moe_plan_contiguous(ids, rows, src, m_indices, k_offsets, first_expert=0,
     m_indices_at = _dense(m_indices, "m_indices", _I32, (m_total,))
     k_offsets_at, ends = _vector(k_offsets, "k_offsets")
     _check("dg_moe_plan_contiguous", _lib.dg_moe_plan_contiguous(
-        ids_at, rows_at, src_at, m_indices_at, k_offsets_at, tokens, topk, int(first_expert), ends - 1, m_total,
-        *_workspace(workspace), _stream(ids)))
+        ids_at, rows_at, src_at, m_indices_at, k_offsets_at, tokens, topk, _int(first_expert, "first_expert"), ends - 1,
+        m_total, *_workspace(workspace), _stream(ids)))
     return rows, src, m_indices, k_offsets
 
 
@@ -287,8 +306,8 @@ def dg_moe_plan_masked(ids, rows, src, masked_m, first_expert=0, workspace=None)
     if groups < 1 or layout_rows % groups:
         raise ValueError("src must hold the same number of rows for every group")
     _check("dg_moe_plan_masked", _lib.dg_moe_plan_masked(
-        ids_at, rows_at, src_at, masked_m_at, tokens, topk, int(first_expert), groups, layout_rows // groups,
-        *_workspace(workspace), _stream(ids)))
+        ids_at, rows_at, src_at, masked_m_at, tokens, topk, _int(first_expert, "first_expert"), groups,
+        layout_rows // groups, *_workspace(workspace), _stream(ids)))
     return rows, src, masked_m
 
 
@@ -311,6 +330,8 @@ def _codes(q, sf, sf_dtypes):
         sf_at, ld = _scales(sf, "sf", sf_dtypes, (groups, cols // 128), rows)
     else:
         raise ValueError("q must have 2 or 3 dimensions")
+    if groups > _MOST or rows > _MOST or cols > _MOST:
+        raise ValueError(f"q of shape {tuple(shape)} has a size of 2^31 or more")
     return q.data_ptr(), sf_at, groups, rows, cols, ld
 
 
@@ -321,7 +342,7 @@ def _dispatch(fn, sf_dtypes, x, src, q, sf, topk):
         raise ValueError("x and q must have the same number of columns")
     src_at = _dense(src, "src", _I32, (groups * rows,))
     _check(fn, _FUNCTIONS[fn](
-        x_at, src_at, q_at, sf_at, tokens, int(topk), cols, rows, groups, ld_x, ld_sf, _stream(x)))
+        x_at, src_at, q_at, sf_at, tokens, _int(topk, "topk"), cols, rows, groups, ld_x, ld_sf, _stream(x)))
     return q, sf
 
 
@@ -355,7 +376,7 @@ def dg_moe_combine(d, rows, y, weights=None):
 
 
 def dg_get_moe_combine_bwd_workspace_size(m_total, cols):
-    return int(_lib.dg_get_moe_combine_bwd_workspace_size(int(m_total), int(cols)))
+    return int(_lib.dg_get_moe_combine_bwd_workspace_size(_int(m_total, "m_total"), _int(cols, "cols")))
 
 
 def dg_moe_combine_bwd(dy, d, src, rows, weights, dq, dsf, dqt, dsft, dweights, workspace=None):

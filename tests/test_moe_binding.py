@@ -71,3 +71,33 @@ def test_calls_refuse_other_workspaces():
     with pytest.raises(ValueError):
         dg.dg_moe_combine_bwd(dy, d, src[:128], ids[:1], w, dq, torch.zeros(1, 128, device="cuda"), None, None, w.clone(),
                               workspace=torch.zeros(512, dtype=torch.uint8))
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    """Sizes go to the library as 32-bit numbers: 2^32 + 5 must not arrive as 5."""
+    import torch
+    from tests.gpu_util import require_gpu
+    dg = require_gpu()
+    n = 2 ** 32 + 5
+    long = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    few = torch.zeros(5, 1, dtype=torch.int32, device="cuda")
+    ids, w = torch.empty(n, 1, dtype=torch.int32, device="cuda"), torch.empty(n, 1, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_route_bf16(long.view(n, 1), ids, w)
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_combine(long.view(1, n), few[:1], long.view(1, n))
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_plan_masked(few, few.clone(), ids.view(-1), few[:1, 0].clone())
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_plan_masked(ids, ids, few[:, 0].clone(), few[:1, 0].clone())
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_swiglu_quant(long.view(1, 1, n), long[:2 ** 31].view(torch.uint8).view(1, 1, 2 ** 32), w.view(-1)[:2 ** 27].view(1, 2 ** 25, 4))
+    x, sf = torch.zeros(8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 8, device="cuda")
+    src, q = torch.zeros(8, dtype=torch.int32, device="cuda"), torch.zeros(8, 128, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_dispatch(x, src, q, sf, topk=2 ** 32 + 1)
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_plan_masked(few, few.clone(), src, few[:1, 0].clone(), first_expert=2 ** 32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_moe_route(torch.zeros(5, 8, device="cuda"), few, torch.zeros(5, 1, device="cuda"), expert_groups=2 ** 32 + 2)
