@@ -361,9 +361,9 @@ __global__ __launch_bounds__(kTileThreads<8>) void combine_bwd_kernel(CombineBwd
   const int64_t row0 = (int64_t)tile.row * kBlockK;
   const int col0 = tile.col * kBlockK;
   const int tid = threadIdx.x, r0 = (tid >> 4) * 8, i16 = tid & 15, c0 = i16 * 8;
-  const TileUse use = tile_use(p.src + row0);
-  if (!use.any()) return;
   const uint32_t entries = (uint32_t)(p.tokens * p.topk);
+  const TileUse use = tile_use(p.src + row0, entries);
+  if (!use.any()) return;
   float vs[1][8][8], w[8];
   auto& v = vs[0];
   uint32_t live = 0;

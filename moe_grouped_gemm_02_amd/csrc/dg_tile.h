@@ -182,8 +182,8 @@ __device__ __forceinline__ int codes_at(int col, int row) {
   return col * kBlockK + (((row >> 4) ^ ((col >> 3) & 7)) * 16) + ((row & 15) ^ ((col >> 6) * 8));
 }
 
-// Rows of the tile in use (index >= 0), the same in every wave: lane l looks at
-// rows l and l + 64.
+// Rows of the tile in use (0 <= index < end), the same in every wave: lane l looks
+// at rows l and l + 64.
 struct TileUse {
   uint64_t lo, hi;
   __device__ __forceinline__ bool any() const { return (lo | hi) != 0; }
@@ -194,11 +194,11 @@ struct TileUse {
     return (uint32_t)((r0 < 64 ? lo : hi) >> (r0 & 63)) & ((1u << R) - 1u);
   }
 };
-__device__ __forceinline__ TileUse tile_use(const int32_t* index) {
+__device__ __forceinline__ TileUse tile_use(const int32_t* index, uint32_t end = 0x80000000u) {
   if (!index) return {~0ull, ~0ull};
   const int lane = threadIdx.x & 63;
-  const int a = index[lane], b = index[lane + 64];
-  return {__ballot(a >= 0), __ballot(b >= 0)};
+  const uint32_t a = (uint32_t)index[lane], b = (uint32_t)index[lane + 64];
+  return {__ballot(a < end), __ballot(b < end)};
 }
 
 // Tile of a workgroup, one of the first row_tiles x column_tiles.  Those
