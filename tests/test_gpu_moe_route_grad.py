@@ -140,3 +140,34 @@ def test_nan_logit_of_a_given_expert_shows(renormalize):
     want = np.zeros((3, 16), dtype=bool)
     want[1, [5, 2, 9] if renormalize else [5]] = True
     assert np.array_equal(np.isnan(got), want)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts,topk,tokens", [(64, 8, 130), (72, 6, 33), (128, 2, 9), (256, 8, 65), (504, 4, 7), (1000, 32, 9), (1024, 8, 5)])
+def test_rows_without_gaps(bf16, score, renormalize, experts, topk, tokens):
+    """Whole vectors of a row's logits: the bits of rows with gaps, and the formula's
+    values to 2^-15 of the largest term."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts + 5 * topk)
+    x = torch.as_tensor(1.5 * rng.standard_normal((tokens, experts)), dtype=torch.float32).bfloat16().float().numpy()
+    x[rng.random(x.shape) < 0.1] = -np.inf
+    ids, _ = moe.route(x, topk, score)
+    ids[0, -1] = -1
+    ids[-1, 0] = experts + 5  # names no expert
+    dw = rng.standard_normal((tokens, topk)).astype(np.float32)
+    got = _bwd(dg, x, ids, dw, bf16, score=score, renormalize=renormalize, scale=2.5)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    wide, gap = (torch.full((tokens, experts + n), float("nan"), dtype=dt, device="cuda") for n in (3, 1))
+    wide[:, :experts] = torch.as_tensor(x, device="cuda")
+    (dg.dg_moe_route_bwd_bf16 if bf16 else dg.dg_moe_route_bwd)(
+        wide[:, :experts], torch.as_tensor(ids, dtype=torch.int32, device="cuda"), torch.as_tensor(dw, device="cuda"),
+        gap[:, :experts], score=score, renormalize=renormalize, scale=2.5)
+    assert np.array_equal(gap[:, :experts].float().cpu().numpy().astype(np.float64), got) and bool(gap[:, experts:].isnan().all())
+    ref = moe.route_bwd(x, ids, dw, score, renormalize, 2.5)
+    s = moe.scores(x, score)
+    chosen = np.where((ids >= 0) & (ids < experts), np.take_along_axis(s, np.clip(ids, 0, experts - 1), 1), 0.0).sum(1, keepdims=True)
+    div = np.where(chosen > 0, chosen, 1.0) if renormalize else 1.0
+    bound = 2.0 ** -15 * 2.5 * np.abs(dw).max(1, keepdims=True) / div * s + 1e-30 + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+    assert np.all(np.abs(got - ref) <= bound)
