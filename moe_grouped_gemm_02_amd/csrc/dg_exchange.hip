@@ -225,10 +225,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanParams p) 
 // ROWS rows at a time, so that their gathered loads are in flight together; which
 // rows and tokens is the same for the whole wave and kept in scalar registers.
 // A token's rows are in different groups, far apart in the walk, so each row of
-// the result is a read of its own: 32768 rows x 7168 of 16384 tokens read 0.45 GB
-// and write 0.23 in 107 us (6.3 TB/s).  The reads alone take 86.  Rows put in token
-// order, so that a token's second read finds it in an L2, gained 5 % and need a
-// sort; 16 lanes a tile lost (135 and more).
+// the result is a read and a quantisation of its own: 32768 rows x 7168 of 16384
+// tokens read 0.45 GB, twice what the tokens hold, and write 0.23 in 107 us (6.3
+// TB/s); the more of a token's choices are in the layout, the more is read again.
+// Rows walked in token order measured the same (124 us against 125 at the time), 16
+// lanes a tile lost (135 and more).
 constexpr int kTilesPerWave = 8;
 constexpr int kRowWaves = 4;
 
@@ -465,9 +466,13 @@ hipError_t launch_dispatch(const DispatchParams& p, bool pow2, hipStream_t strea
   const int gx = (p.cols / kBlockK + kTilesPerWave - 1) / kTilesPerWave;
   const int64_t total = (int64_t)p.groups * p.rows;
   // Tall layouts are streams, which four rows of a wave at a time and streaming
-  // stores suit (32768 x 7168: 115 us, and 124 row by row with plain stores); short
-  // ones wait for their reads, which more waves share (128 tokens in 32 groups of
-  // 128 rows: 4.8 us, and 5.7 by four; 8192 rows: a call in 21.9 and 22.8).
+  // stores suit, whatever their width (32768 x 7168: 103 us, 116 with plain stores
+  // and 127 with those row by row; 16384 x 1024: 8.2, 10.4 and 9.8; only very narrow
+  // ones lose, 16384 x 128: 7.9, 7.9 and 6.9), and few rows in use go both ways (32
+  // groups of 1024 rows, 3 % in use: 12.0 us against 10.1 row by row; 64 groups, 6 %:
+  // 15.5 and 24.1).  Short ones wait for their reads, which more waves share (128
+  // tokens in 32 groups of 128 rows: 4.8 us, and 5.7 by four; 8192 rows: a call in
+  // 21.9 and 22.8).
   const int rows = total >= 16384 ? 4 : 1;
   // Tall: most waves make one trip (107 us, 114 with up to four trips).  Short: up
   // to two (8192 rows: a call in 23.6, 24.3 with one).
