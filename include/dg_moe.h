@@ -67,9 +67,9 @@ enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 };
  *   w_j   = scale * s_ids[j] / sum_i s_ids[i]   (renormalize != 0), or
  *           scale * s_ids[j].
  * Equal keys, and equal group scores, go to the lowest index.  An expert
- * whose logit is -inf is masked: it is never chosen and adds nothing to its
- * group's score, and a group of masked experts is never chosen.  Slots left
- * without an expert get id -1 and weight 0 (all of them, in a row whose
+ * whose logit or bias is -inf is masked: it is never chosen and adds nothing
+ * to its group's score, and a group of masked experts is never chosen.  Slots
+ * left without an expert get id -1 and weight 0 (all of them, in a row whose
  * experts are all masked).  A key that is NaN is never chosen; a NaN logit
  * makes every softmax score of its token NaN, which then shows in its weights
  * or, where the keys hold scores, leaves the token without experts.

@@ -43,6 +43,24 @@ def test_combine_bwd_leaves_blocks_of_rows_that_name_no_entry():
     check_transposed(host(dqt), host(dsft), ref, live, cols)
 
 
+# ------------------------------------------------------------------ routing --
+
+@pytest.mark.parametrize("groups,keep,group_top", [(1, 1, 2), (4, 2, 2), (4, 2, 1), (8, 3, 2), (16, 5, 2)])
+def test_infinite_biases(groups, keep, group_top):
+    """A bias of -inf masks its expert like a logit of -inf, one of +inf puts it first."""
+    dg = require_gpu()
+    rng = np.random.default_rng(groups)
+    x = np.stack([rng.permutation(16) * 0.25 - 2.0 for _ in range(40)]).astype(np.float32)
+    bias = np.zeros(16, dtype=np.float32)
+    bias[[1, 2, 3, 8, 13]], bias[6] = -np.inf, np.inf
+    ids, w = torch.empty(40, 4, dtype=torch.int32, device="cuda"), torch.empty(40, 4, device="cuda")
+    dg.dg_moe_route(torch.as_tensor(x, device="cuda"), ids, w, bias=torch.as_tensor(bias, device="cuda"), score="sigmoid",
+                    expert_groups=groups, topk_groups=keep, group_top=group_top)
+    ref, ref_w = moe.route(x, 4, "sigmoid", bias, groups, keep, group_top)
+    assert np.array_equal(host(ids), ref) and np.all(ref[:, 0] == 6) and not np.isin(ref, [1, 2, 3, 8, 13]).any()
+    assert np.all(np.abs(host(w) - ref_w) <= 2.0 ** -18 * ref_w)
+
+
 # ------------------------------------------------------- the unit's backward --
 
 def _used(m_total, seed, empty):

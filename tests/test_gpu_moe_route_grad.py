@@ -171,3 +171,18 @@ def test_rows_without_gaps(bf16, score, renormalize, experts, topk, tokens):
     div = np.where(chosen > 0, chosen, 1.0) if renormalize else 1.0
     bound = 2.0 ** -15 * 2.5 * np.abs(dw).max(1, keepdims=True) / div * s + 1e-30 + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
     assert np.all(np.abs(got - ref) <= bound)
+
+
+@pytest.mark.parametrize("experts,topk", [(4, 4), (72, 6), (256, 8)])
+@pytest.mark.parametrize("low,high", [(-97.0, -88.0), (-87.0, -60.0)])
+def test_weights_of_tiny_sigmoids(low, high, experts, topk):
+    """The weights whose gradient test_tiny_sigmoids takes, to the same accuracy."""
+    dg = require_gpu()
+    rng = np.random.default_rng(experts + topk)
+    x = rng.uniform(low, high, (33, experts)).astype(np.float32)
+    ref_ids, ref = moe.route(x, topk, "sigmoid", scale=2.5)
+    ids, w = torch.empty(33, topk, dtype=torch.int32, device="cuda"), torch.empty(33, topk, device="cuda")
+    dg.dg_moe_route(torch.as_tensor(x, device="cuda"), ids, w, score="sigmoid", scale=2.5)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    total = np.take_along_axis(moe.scores(x, "sigmoid"), ref_ids, 1).sum(1, keepdims=True)
+    assert np.all(np.abs(w.cpu().numpy() - ref) <= 2.0 ** -17 * ref + 2.5 * (topk + 1) * 2.0 ** -149 / total)
