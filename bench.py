@@ -548,7 +548,7 @@ def _cpu_model():
 # reports it only while the sources are unchanged.
 
 PROFILES = os.path.join(os.path.dirname(os.path.abspath(__file__)), "profiles")
-KERNEL_SOURCES = ("dg_gemm.hip", "dg_device.h", "dg_internal.h")
+KERNEL_SOURCES = ("dg_gemm.hip", "dg_gemm_kernel.h", "dg_device.h", "dg_internal.h")
 COPY_BYTES = 256 << 20
 
 

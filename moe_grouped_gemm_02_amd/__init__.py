@@ -558,3 +558,7 @@ def raw():
 # The operators around the grouped GEMMs in a mixture-of-experts layer
 # (include/dg_moe.h): routing, the token exchange, 8-bit checkpoints.
 from .moe import *  # noqa: E402,F401,F403
+
+# The operators of a transformer block around the products (include/dg_block.h):
+# norms with gate and residual, the router's balance, the GEMM with an epilogue.
+from .block import *  # noqa: E402,F401,F403

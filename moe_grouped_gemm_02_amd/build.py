@@ -35,7 +35,8 @@ ASAN_LIB = os.path.join(HERE, "libdg_host_asan.so")
 PROBE_LIB = os.path.join(HERE, "libdg_probe.so")
 PROBE_SOURCES = ["dg_probe.hip"]
 SOURCES = ["dg_api.hip", "dg_quant.hip", "dg_gemm.hip",
-           "dg_moe_api.hip", "dg_route.hip", "dg_exchange.hip", "dg_ckpt.hip"]
+           "dg_moe_api.hip", "dg_route.hip", "dg_exchange.hip", "dg_ckpt.hip",
+           "dg_block_api.hip", "dg_norm.hip", "dg_balance.hip", "dg_gemm_epilogue.hip", "dg_epilogue_bwd.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

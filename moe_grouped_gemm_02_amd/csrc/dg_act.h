@@ -1,0 +1,61 @@
+// Activation functions of a product's epilogue and their slopes, in float32,
+// and the rounding of a pair of values to bf16.
+#pragma once
+
+#include <type_traits>
+
+#include "dg_block.h"
+#include "dg_math.h"
+#include "dg_tile.h"
+
+namespace dg {
+
+// Two values rounded to bf16 (to nearest even, NaN quiet), the first one low.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2b));
+}
+
+// The tanh form of the GELU is z / (1 + e^-t), t = 2 sqrt(2 / pi) (z + 0.044715 z^3):
+// (1 + tanh(u)) / 2 is the sigmoid of 2 u, which keeps its relative accuracy
+// for negative z.
+constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.071354816272600247f;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == DG_ACT_RELU) return z < 0.0f ? 0.0f : z;
+  else if constexpr (ACT == DG_ACT_SILU) return z * sigmoid(z).sig;
+  else if constexpr (ACT == DG_ACT_GELU_TANH) return z * sigmoid(z * fmaf(kGelu3, z * z, kGelu1)).sig;
+  else return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == DG_ACT_RELU) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == DG_ACT_SILU) {
+    return silu_slope(z, 1.0f, z, sigmoid(z));
+  } else if constexpr (ACT == DG_ACT_GELU_TANH) {
+    // Past +-12 the slope is 1 or below 2^-126; t stays within the exponential's
+    // range up to there and z^2 finite.
+    const float v = __builtin_amdgcn_fmed3f(z, -12.0f, 12.0f), v2 = v * v;
+    const Sigmoid s = sigmoid(v * fmaf(kGelu3, v2, kGelu1));
+    return s.sig * fmaf(v * s.n, fmaf(3.0f * kGelu3, v2, kGelu1), 1.0f);
+  } else {
+    return 1.0f;
+  }
+}
+
+// f with the activation as a type.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case DG_ACT_RELU: f(std::integral_constant<int, DG_ACT_RELU>{}); break;
+    case DG_ACT_SILU: f(std::integral_constant<int, DG_ACT_SILU>{}); break;
+    case DG_ACT_GELU_TANH: f(std::integral_constant<int, DG_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, DG_ACT_NONE>{}); break;
+  }
+}
+
+}  // namespace dg

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "dg.h"
+#include "dg_block.h"
 #include "dg_internal.h"
 #include "dg_status.h"
 
@@ -117,7 +118,7 @@ int check_workspace(const dg::GemmConfig& cfg, int layout, int rows, int n, int 
 }
 
 int run_gemm(int layout, dg::GemmParams& p, int rows, int groups, void* ws, size_t ws_bytes,
-             void* stream, int expected_m = 0) {
+             void* stream, int expected_m = 0, const dg::GemmEpilogue* epi = nullptr) {
   if (!dg::plannable(layout, rows, p.n, groups))
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "too many output tiles (m=%d n=%d groups=%d)", rows, p.n, groups);
   const int cus = resolve_num_cus();
@@ -131,6 +132,8 @@ int run_gemm(int layout, dg::GemmParams& p, int rows, int groups, void* ws, size
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "tile variant %d is not built for MN-major operands", cfg.variant);
   if (p.sf_ue8m0 && !dg::ue8m0_variant_built(cfg.variant))
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "tile variant %d is not built for UE8M0 scales", cfg.variant);
+  if (epi && !dg::epilogue_variant_built(cfg.variant, p.sf_ue8m0 != 0))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "tile variant %d is not built with an epilogue", cfg.variant);
   if (qout && !dg::variant_quantises_output(cfg.variant))
     return fail(DG_ERR_UNSUPPORTED_SHAPE, "tile variant %d cannot quantise its output (columns not whole 128-blocks)",
                 cfg.variant);
@@ -142,7 +145,8 @@ int run_gemm(int layout, dg::GemmParams& p, int rows, int groups, void* ws, size
     fprintf(stderr, "[dg] %s m=%d n=%d k=%d groups=%d: bm=%d bn=%d stream_k=%d grid=%d tiles=%d variant=%d cus=%d\n",
             layout_name(layout), rows, p.n, p.k, groups, cfg.bm, cfg.bn, cfg.stream_k, cfg.grid,
             cfg.tiles, cfg.variant, cus);
-  const hipError_t e = dg::launch_gemm(layout, p, cfg, static_cast<hipStream_t>(stream));
+  const hipError_t e = epi ? dg::launch_gemm_epilogue(p, *epi, cfg, static_cast<hipStream_t>(stream))
+                           : dg::launch_gemm(layout, p, cfg, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(DG_ERR_HIP, "GEMM launch failed: %s", hipGetErrorString(e));
   return ok();
 }
@@ -169,6 +173,19 @@ int check_qout(const QOut* q, int rows, int n, int groups) {
   return DG_SUCCESS;
 }
 
+int check_epilogue(const dg::GemmEpilogue& e, int m, int n) {
+  if (e.act < DG_ACT_NONE || e.act > DG_ACT_GELU_TANH) return fail(DG_ERR_INVALID_VALUE, "act=%d is not an activation", e.act);
+  if (!aligned16(e.residual) || !aligned16(e.pre)) return fail(DG_ERR_MISALIGNED, "residual and pre must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(e.bias) % 4) return fail(DG_ERR_MISALIGNED, "bias must be 4-byte aligned");
+  if ((e.residual && e.ld_res < n) || (e.pre && e.ld_pre < n)) return fail(DG_ERR_INVALID_VALUE, "ld_res or ld_pre smaller than n");
+  if ((e.residual && e.ld_res % 8) || (e.pre && e.ld_pre % 8))
+    return fail(DG_ERR_MISALIGNED, "ld_res and ld_pre must be multiples of 8 elements");
+  const int64_t lim = (int64_t)1 << 46;
+  if ((e.residual && !below(m, e.ld_res, 2, lim)) || (e.pre && !below(m, e.ld_pre, 2, lim)))
+    return fail(DG_ERR_UNSUPPORTED_SHAPE, "residual or pre too large");
+  return DG_SUCCESS;
+}
+
 void set_qout(dg::GemmParams& p, const QOut* q, int rows, int n) {
   if (!q) return;
   p.dq = q->dq;
@@ -192,9 +209,12 @@ void set_scales(dg::GemmParams& p, const void* sfa, const void* sfb, int n, int 
 int gemm_nt_impl(const uint8_t* a, const void* sfa, const uint8_t* b, const void* sfb, uint16_t* d,
                  int m, int n, int k, int64_t lda, int64_t ldb, int64_t ldd, int64_t ld_sfa,
                  void* workspace, size_t workspace_bytes, void* stream, bool ue8m0,
-                 const QOut* qo = nullptr) {
+                 const QOut* qo = nullptr, const dg::GemmEpilogue* epi = nullptr) {
+  // An empty output of a caller's allocator may have no address.
+  if (epi && (m == 0 || n == 0) && m >= 0 && n >= 0 && k >= 0 && k % 128 == 0) return ok();
   int st = check_gemm_common(a, sfa, b, sfb, d, m, n, k, lda, ldb, ldd, ld_sfa);
   if (st == DG_SUCCESS) st = check_qout(qo, m, n, 1);
+  if (st == DG_SUCCESS && epi) st = check_epilogue(*epi, m, n);
   if (st != DG_SUCCESS) return st;
   if (m == 0 || n == 0) return ok();
   dg::GemmParams p{};
@@ -203,7 +223,7 @@ int gemm_nt_impl(const uint8_t* a, const void* sfa, const uint8_t* b, const void
   set_qout(p, qo, m, n);
   p.m = m; p.n = n; p.k = k; p.num_groups = 1;
   p.lda = lda; p.ldb = ldb; p.ldd = ldd; p.ld_sfa = ld_sfa;
-  return run_gemm(dg::kDense, p, m, 1, workspace, workspace_bytes, stream);
+  return run_gemm(dg::kDense, p, m, 1, workspace, workspace_bytes, stream, 0, epi);
 }
 
 // Dense GEMM with MN-major operands.  majors bit 0: A is stored M-major as
@@ -613,6 +633,27 @@ int dg_quant_128x128_ue8m0(const uint16_t* w, uint8_t* q, uint8_t* sf, int rows,
 int64_t dg_get_ue8m0_sfb_leading_dim(int n) {
   if (n < 0) return -1;
   return (((int64_t)n + 127) / 128 + 3) / 4 * 4;
+}
+
+int dg_fp8_gemm_nt_epilogue(const uint8_t* a, const float* sfa, const uint8_t* b, const float* sfb, const float* bias,
+                            const uint16_t* residual, uint16_t* d, uint16_t* pre, uint8_t* dq, float* dsf, int m, int n,
+                            int k, int64_t lda, int64_t ldb, int64_t ldd, int64_t ld_sfa, int64_t ld_res, int64_t ld_pre,
+                            int64_t ld_dsf, int act, void* workspace, size_t workspace_bytes, void* stream) {
+  const QOut q{dq, dsf, ld_dsf, false};
+  const dg::GemmEpilogue e{bias, residual, pre, ld_res, ld_pre, act};
+  return gemm_nt_impl(a, sfa, b, sfb, d, m, n, k, lda, ldb, ldd, ld_sfa, workspace, workspace_bytes, stream, false,
+                      dq || dsf ? &q : nullptr, &e);
+}
+
+int dg_fp8_gemm_nt_ue8m0_epilogue(const uint8_t* a, const uint8_t* sfa, const uint8_t* b, const uint8_t* sfb,
+                                  const float* bias, const uint16_t* residual, uint16_t* d, uint16_t* pre, uint8_t* dq,
+                                  uint8_t* dsf, int m, int n, int k, int64_t lda, int64_t ldb, int64_t ldd,
+                                  int64_t ld_sfa, int64_t ld_res, int64_t ld_pre, int64_t ld_dsf, int act,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  const QOut q{dq, dsf, ld_dsf, true};
+  const dg::GemmEpilogue e{bias, residual, pre, ld_res, ld_pre, act};
+  return gemm_nt_impl(a, sfa, b, sfb, d, m, n, k, lda, ldb, ldd, ld_sfa, workspace, workspace_bytes, stream, true,
+                      dq || dsf ? &q : nullptr, &e);
 }
 
 size_t dg_get_workspace_size(int m, int n, int k, int num_groups) {

@@ -1,0 +1,332 @@
+// Load balance of a router over sequences for gfx950: the experts' counts and
+// the loss in two launches, the gradient in one.
+//
+// A wave holds a token's logits, lane l experts V l .. V l + V - 1.  A workgroup
+// has a chunk of consecutive tokens, finds the sequence of its first one and walks
+// from sequence to sequence.  Forward it leaves, for every sequence that meets the
+// chunk, a row of sums over their common tokens: chunk b and sequence s share row
+// b + s (both only grow along the tokens, so no two pairs have the same), and a
+// second launch adds the rows of each sequence in their order.
+
+#include "dg_block_internal.h"
+#include "dg_math.h"
+#include "dg_moe_internal.h"
+#include "dg_route_rows.h"
+
+namespace dg {
+namespace {
+
+constexpr int kWaves = 4;
+
+// Sequence ends, brought into [0, tokens].
+struct Sequences {
+  const int32_t* offsets;
+  int count, tokens;
+  __device__ __forceinline__ int at(int s) const {
+    if (!offsets) return s == 0 ? 0 : tokens;
+    return min(max(offsets[s], 0), tokens);
+  }
+  // The first sequence that ends behind token t (count: none).
+  __device__ __forceinline__ int of(int t) const {
+    int lo = 0, hi = count;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (at(mid + 1) > t) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  }
+};
+
+// f(s, from, to) for each sequence s with tokens in [t0, t1), and those; uniform.
+// `from` grows with every turn whatever the offsets hold: the sequence that is
+// found ends behind it.
+template <typename F>
+__device__ __forceinline__ void for_sequences(const Sequences& q, int t0, int t1, F&& f) {
+  int t = t0;
+  while (t < t1) {
+    const int s = q.of(t);
+    if (s >= q.count) return;
+    const int begin = q.at(s);
+    if (begin > t) {
+      t = begin;
+      continue;
+    }
+    const int end = min(q.at(s + 1), t1);
+    f(s, t, end);
+    t = end;
+  }
+}
+
+// Shares p of the wave's token, and for sigmoid scores 1 minus the score (1 for
+// softmax).  Scores are taken relative to the largest one where all are small, so
+// that tokens whose scores leave float32 have shares like any other.  True where
+// some logit is not -inf.
+template <int V>
+__device__ __forceinline__ bool shares(const float (&x)[V], float (&p)[V], float (&rest)[V], bool sigmoid_scores) {
+  uint32_t most = 0;
+  bool open = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    most = umax(most, order_of(x[i]));
+    open |= !(x[i] == -INFINITY);
+  }
+  most = wave_max(most);
+  const float top = most ? of_order(most) : 0.0f;
+  float total = 0.0f;
+  if (sigmoid_scores) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) both_sigmoids(x[i], p[i], rest[i]);
+    if (top < 0.0f) {  // s_e / s_max up to a factor that cancels: e^(x - top) (1 - s)
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = exp_to_80(x[i] - top) * rest[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += p[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float d = x[i] - top, e = exp_to_80(d);
+      p[i] = d == d ? e : d;
+      rest[i] = 1.0f;
+      total += p[i];
+    }
+  }
+  total = wave_sum(total);
+  const float inv = total == 0.0f ? 0.0f : reciprocal(total);
+#pragma unroll
+  for (int i = 0; i < V; ++i) p[i] *= inv;
+  return __ballot(open) != 0;
+}
+
+template <bool VEC, typename T, int V>
+__global__ __launch_bounds__(64 * kWaves) void balance_kernel(BalanceParams p) {
+  __shared__ float sums[kWaves][64 * V];
+  __shared__ int counts[64 * V];
+  __shared__ int used[kWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0;
+  const Sequences seqs = {p.offsets, p.seqs, p.tokens};
+  const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = t0 + p.chunk;
+  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), [&](int s, int from, int to) {
+    for (int e = threadIdx.x; e < p.experts; e += 64 * kWaves) counts[e] = 0;
+    __syncthreads();
+    float sum[V] = {};
+    int here = 0;
+    for (int t = from + wave; t < to; t += kWaves) {
+      float x[V], share[V], rest[V];
+      load_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, sums[wave], x);
+      const int id = lane < p.topk ? p.ids[(int64_t)t * p.topk + lane] : -1;
+      if (!shares<V>(x, share, rest, p.sigmoid != 0)) continue;
+      ++here;
+      if (id >= 0 && id < p.experts) atomicAdd(&counts[id], 1);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += share[i];
+    }
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
+    if (lane == 0) used[wave] = here;
+    __syncthreads();
+    const int64_t row = (int64_t)blockIdx.x + s;
+    for (int e = threadIdx.x; e < p.experts; e += 64 * kWaves) {
+      p.share_parts[row * p.experts + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+      p.count_parts[row * p.experts + e] = counts[e];
+    }
+    if (threadIdx.x == 0) p.used_parts[row] = used[0] + used[1] + used[2] + used[3];
+    __syncthreads();
+  });
+}
+
+// Workgroup (s, y): 64 experts of sequence s, ROWS threads for each, which share the
+// rows of the sequence's chunks.  The last workgroup to arrive adds up the loss; it
+// reads what the others left past its own L2.
+constexpr int kExperts = 64;
+
+template <int ROWS>
+__global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalanceParams p) {
+  __shared__ float shares[ROWS][kExperts];
+  __shared__ int counts[ROWS][kExperts];
+  __shared__ int used_sum;
+  __shared__ bool last;
+  constexpr int kThreads = kExperts * ROWS;
+  const int tid = threadIdx.x, at = tid % kExperts, part = tid / kExperts;
+  const int s = blockIdx.x, e = blockIdx.y * kExperts + at;
+  const Sequences seqs = {p.offsets, p.seqs, p.tokens};
+  const int begin = seqs.at(s), end = seqs.at(s + 1);
+  const int64_t first = begin / p.chunk, rows = end > begin ? (end - 1) / p.chunk - first + 1 : 0;
+  if (tid == 0) used_sum = 0;
+  __syncthreads();
+  float share = 0.0f;
+  int count = 0, used = 0;
+  if (e < p.experts) {
+#pragma unroll 8
+    for (int64_t r = part; r < rows; r += ROWS) {
+      const int64_t from = (first + s + r) * p.experts + e;
+      share += p.share_parts[from];
+      count += p.count_parts[from];
+    }
+  }
+  for (int64_t r = tid; r < rows; r += kThreads) used += p.used_parts[first + s + r];
+  if (used) atomicAdd(&used_sum, used);
+  shares[part][at] = share, counts[part][at] = count;
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int k = 1; k < ROWS; ++k) share += shares[k][at], count += counts[k][at];
+    used = used_sum;
+    const float n = (float)used;
+    // f_e P_e = experts c_e / (topk n) times share / n
+    const float f = used ? (float)p.experts * (float)count / ((float)p.topk * n) : 0.0f;
+    const float product = e < p.experts && used ? f * (share / n) : 0.0f;
+    if (e < p.experts) p.counts[(int64_t)s * p.experts + e] = count;
+    if (e == 0) p.used[s] = used;
+    const float sum = wave_sum(product);
+    if (at == 0) {
+      __hip_atomic_store(&p.loss_parts[(int64_t)s * gridDim.y + blockIdx.y], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __threadfence();
+      last = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  float sum = 0.0f;
+  for (int64_t k = tid; k < (int64_t)gridDim.x * gridDim.y; k += kThreads)
+    sum += __hip_atomic_load(&p.loss_parts[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = wave_sum(sum);
+  if (at == 0) shares[part][0] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    for (int k = 1; k < ROWS; ++k) sum += shares[k][0];
+    *p.loss = p.coef * (sum / (float)p.seqs);
+  }
+}
+
+constexpr int kBwdChunk = 16;  // tokens of a workgroup
+
+template <bool VEC, typename T, int V>
+__global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams p) {
+  __shared__ float rows[kWaves][64 * V];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Sequences seqs = {p.offsets, p.seqs, p.tokens};
+  const float dloss = p.dloss ? *p.dloss : 1.0f;
+  const int64_t t0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kBwdChunk, t1 = t0 + kBwdChunk;
+  if (t0 >= p.tokens) return;
+  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), [&](int s, int from, int to) {
+    const int used = p.used[s];
+    const float n = (float)used;
+    const float a = used > 0 ? dloss * p.coef / ((float)p.seqs * n) : 0.0f;
+    const float per = used > 0 ? (float)p.experts / ((float)p.topk * n) : 0.0f;
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      f[i] = e < p.experts ? per * (float)p.counts[(int64_t)s * p.experts + e] : 0.0f;
+    }
+    for (int t = from + wave; t < to; t += kWaves) {
+      float x[V], add[V], share[V], rest[V];
+      load_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, rows[wave], x);
+      if (p.add) load_row<VEC>(static_cast<const T*>(p.add) + (int64_t)t * p.ld_add, p.experts, lane, rows[wave], add);
+      shares<V>(x, share, rest, p.sigmoid != 0);
+      float mean = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) mean = fmaf(f[i], share[i], mean);
+      mean = wave_sum(mean);
+      float out[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        out[i] = a * (share[i] * rest[i] * (f[i] - mean));
+        if (p.add) out[i] += add[i];
+      }
+      T* to_row = static_cast<T*>(p.dlogits) + (int64_t)t * p.ld_d;
+      if constexpr (VEC) {
+        Pack<T, V> pack;
+#pragma unroll
+        for (int i = 0; i < V; ++i) narrow(pack.v[i], out[i]);
+        if (lane * V < p.experts) *reinterpret_cast<Pack<T, V>*>(to_row + lane * V) = pack;
+      } else {
+        wave_fence();
+#pragma unroll
+        for (int i = 0; i < V; ++i) rows[wave][lane * V + i] = out[i];
+        wave_fence();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = i * 64 + lane;
+          if (e < p.experts) narrow(to_row[e], rows[wave][e]);
+        }
+      }
+    }
+  });
+}
+
+template <bool VEC, typename T, int V>
+void go(const BalanceParams& p, bool bwd, hipStream_t stream) {
+  const dim3 block(64 * kWaves);
+  if (bwd) {
+    const GridXY grid = spread(((int64_t)p.tokens + kBwdChunk - 1) / kBwdChunk);
+    hipLaunchKernelGGL((balance_bwd_kernel<VEC, T, V>), dim3(grid.x, grid.y), block, 0, stream, p);
+  } else {
+    const int64_t chunks = ((int64_t)p.tokens + p.chunk - 1) / p.chunk;
+    hipLaunchKernelGGL((balance_kernel<VEC, T, V>), dim3((unsigned)(chunks > 0 ? chunks : 1)), block, 0, stream, p);
+  }
+}
+
+// Whole vectors: no ragged last lane, and every row starts on a vector.
+template <typename T, int V>
+void go(const BalanceParams& p, bool bwd, hipStream_t stream) {
+  constexpr size_t kAlign = alignof(Pack<T, V>);
+  auto fits = [&](const void* at, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(at) % kAlign == 0 && ld * sizeof(T) % kAlign == 0;
+  };
+  const bool vec = p.experts % V == 0 && fits(p.logits, p.ld) &&
+                   (!bwd || (fits(p.dlogits, p.ld_d) && (!p.add || fits(p.add, p.ld_add))));
+  if (vec) go<true, T, V>(p, bwd, stream);
+  else go<false, T, V>(p, bwd, stream);
+}
+
+template <typename T>
+void pick(const BalanceParams& p, bool bwd, hipStream_t stream) {
+  const int v = (p.experts + 63) / 64;
+  if (v <= 1) go<T, 1>(p, bwd, stream);
+  else if (v <= 2) go<T, 2>(p, bwd, stream);
+  else if (v <= 4) go<T, 4>(p, bwd, stream);
+  else if (v <= 8) go<T, 8>(p, bwd, stream);
+  else go<T, 16>(p, bwd, stream);
+}
+
+}  // namespace
+
+int balance_chunk(int tokens) {
+  // At most 65536 chunks.
+  const int64_t least = ((int64_t)tokens + 65535) / 65536;
+  return (int)(least > 32 ? least : 32);
+}
+
+int64_t balance_slots(int tokens, int seqs) {
+  const int64_t chunk = balance_chunk(tokens);
+  return ((int64_t)tokens + chunk - 1) / chunk + seqs;
+}
+
+int balance_loss_parts(int experts) { return (experts + kExperts - 1) / kExperts; }
+
+hipError_t launch_balance(const BalanceParams& p, bool bf16, hipStream_t stream) {
+  if (bf16) pick<uint16_t>(p, false, stream);
+  else pick<float>(p, false, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid(p.seqs, balance_loss_parts(p.experts));
+  const int64_t chunks_of_one = ((int64_t)p.tokens / p.seqs) / p.chunk;
+  if (chunks_of_one > 16) hipLaunchKernelGGL(balance_sum_kernel<16>, grid, dim3(kExperts * 16), 0, stream, p);
+  else hipLaunchKernelGGL(balance_sum_kernel<4>, grid, dim3(kExperts * 4), 0, stream, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_bwd(const BalanceParams& p, bool bf16, hipStream_t stream) {
+  if (bf16) pick<uint16_t>(p, true, stream);
+  else pick<float>(p, true, stream);
+  return hipGetLastError();
+}
+
+}  // namespace dg

@@ -8,6 +8,16 @@ namespace dg {
 
 enum Layout : int { kDense = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3 };
 
+// What an epilogue does to the sums before they are rounded (dense layout):
+// z = sum + bias, d = act(z) + residual.
+struct GemmEpilogue {
+  const float* bias;         // [n], null: none
+  const uint16_t* residual;  // [m][ld_res] bf16, null: none
+  uint16_t* pre;             // [m][ld_pre] bf16 of z, null: not wanted
+  int64_t ld_res, ld_pre;
+  int act;                   // DG_ACT_*
+};
+
 // Everything a GEMM kernel needs; group strides are in elements.
 struct GemmParams {
   const uint8_t* a;
@@ -53,6 +63,12 @@ inline bool kgrouped_variant_built(int variant) {
 // Tile variants built with MN-major operands.
 inline bool majors_variant_built(int variant) {
   return variant == 0 || variant == 4 || variant == 5 || variant == 6;
+}
+
+// Tile variants built with an epilogue: those that choose_config() picks for
+// the dense layout.
+inline bool epilogue_variant_built(int variant, bool ue8m0) {
+  return variant == 0 || variant == 4 || variant == 5 || variant == 6 || (variant == 11 && !ue8m0);
 }
 
 inline bool ue8m0_variant_built(int variant) {
@@ -108,10 +124,14 @@ GemmConfig choose_config(int layout, int m, int n, int k, int groups, int num_cu
                          bool qout = false, bool narrow_ok = true);
 // Whether a tile variant's columns are whole 128-column blocks.
 bool variant_quantises_output(int variant);
+// The schedule of a configuration's launch.
+Schedule schedule_of(int layout, const GemmParams& p, const GemmConfig& cfg);
 size_t workspace_bytes_for(const GemmConfig& cfg, int layout, int m, int n, int groups);
 
 hipError_t launch_gemm(int layout, const GemmParams& p, const GemmConfig& cfg,
                        hipStream_t stream);
+// The dense GEMM with an epilogue (variants epilogue_variant_built).
+hipError_t launch_gemm_epilogue(const GemmParams& p, const GemmEpilogue& e, const GemmConfig& cfg, hipStream_t stream);
 // pow2: UE8M0 exponent bytes instead of fp32 scales (see dg_quant.hip).
 hipError_t launch_quant_1x128(const uint16_t* x, uint8_t* q, void* sf, int rows, int cols,
                               int64_t ld_sf, int groups, bool pow2, hipStream_t stream);

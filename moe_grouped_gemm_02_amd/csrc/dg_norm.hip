@@ -1,0 +1,532 @@
+// The junction of two transformer blocks for gfx950: the norm after a block,
+// gate and residual scale, the norm before the next block with the next GEMM's
+// operand as its result, and the gradient of all of it.
+//
+// A team of threads (a wave, or a workgroup) holds one row, thread i chunks i,
+// i + TEAM, .. of 8 values, so that loads and stores are whole 16-byte vectors
+// side by side, 16 lanes own the 128 values of a code tile, and a row is read
+// once, whatever its norms need: statistics are sums over the team, by row
+// operations inside a wave and through shared memory between waves.
+
+#include "dg_act.h"
+#include "dg_block_internal.h"
+#include "dg_math.h"
+#include "dg_tile.h"
+
+namespace dg {
+namespace {
+
+__device__ __forceinline__ void widen8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f[2 * c] = __uint_as_float(w[c] << 16);
+    f[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
+  return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// 1 / sqrt(a) for normal a: the hardware's (1 ulp) and one Newton step.
+__device__ __forceinline__ float inverse_root(float a) {
+  const float y = __builtin_amdgcn_rsqf(a);
+  return fmaf(y * 0.5f, fmaf(-a * y, y, 1.0f), y);
+}
+
+// Sums over a team of N values each.  Two calls one after another use different
+// words of shared memory (`turn`), so that one barrier a call is enough: the words
+// of a call are written again behind the barrier of the next one, which every wave
+// passes after it has read them.
+template <int TEAM>
+struct TeamSums {
+  static constexpr int kWaves = TEAM / 64;
+  float words[2][kWaves][4];
+};
+
+template <int TEAM, int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], TeamSums<TEAM>& lds, int& turn) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+  if constexpr (TEAM > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) lds.words[turn][wave][n] = v[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float sum = lds.words[turn][0][n];
+#pragma unroll
+      for (int w = 1; w < TEAM / 64; ++w) sum += lds.words[turn][w][n];
+      v[n] = sum;
+    }
+    turn ^= 1;
+  }
+}
+
+// The thread's chunks of a row.
+template <int TEAM, int V>
+struct Chunks {
+  int lane, count;  // place in the team; chunks of the row
+  __device__ __forceinline__ int at(int i) const { return i * TEAM + lane; }
+  // Only the last of a thread's chunks can lie past the row's end (the host picks the
+  // least V).
+  __device__ __forceinline__ bool in(int i) const { return i < V - 1 || at(i) < count; }
+};
+
+template <int TEAM, int V>
+__device__ __forceinline__ void load_chunks(const uint16_t* row, const Chunks<TEAM, V>& c, uint4 (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = c.in(i) ? load_streaming4(row + c.at(i) * 8) : make_uint4(0, 0, 0, 0);
+}
+
+template <int TEAM, int V>
+__device__ __forceinline__ void store_chunks(uint16_t* row, const Chunks<TEAM, V>& c, const float (&v)[V][8]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c.in(i)) *reinterpret_cast<uint4*>(row + c.at(i) * 8) = narrow8(v[i]);
+}
+
+// v = f(v, w) with the chunk's columns of w, f(v, 1) without w left out.
+template <int TEAM, int V, typename F>
+__device__ __forceinline__ void with_columns(const float* w, const Chunks<TEAM, V>& c, float (&v)[V][8], F&& f) {
+  if (!w) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (!c.in(i)) continue;
+    float k[8];
+    load8(w + c.at(i) * 8, k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = f(v[i][e], k[e]);
+  }
+}
+
+// v = norm(v), without weights.  Layer norms take the mean first and the squares
+// of what is left: a single pass would lose rows with a large mean.
+template <int TEAM, int V>
+__device__ __forceinline__ void normalise(float (&v)[V][8], const Chunks<TEAM, V>& c, bool layer, float inv_cols, float eps,
+                                          TeamSums<TEAM>& lds, int& turn) {
+  if (layer) {
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += v[i][e];
+    team_sums<TEAM>(sum, lds, turn);
+    const float mean = sum[0] * inv_cols;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = c.in(i) ? v[i][e] - mean : 0.0f;
+  }
+  float squares[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) squares[0] = fmaf(v[i][e], v[i][e], squares[0]);
+  team_sums<TEAM>(squares, lds, turn);
+  const float k = inverse_root(fmaf(squares[0], inv_cols, eps));
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] *= k;
+}
+
+// Threads of a workgroup: teams smaller than 256 threads share one.
+template <int TEAM>
+constexpr int kNormThreads = TEAM < 256 ? 256 : TEAM;
+
+template <bool POW2, int TEAM, int V>
+__global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) {
+  constexpr int kTeams = kNormThreads<TEAM> / TEAM;
+  static_assert(kTeams == 1 || TEAM == 64, "teams that share a workgroup are waves");
+  __shared__ TeamSums<TEAM> lds;
+  int turn = 0;
+  const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
+  const float inv_cols = 1.0f / (float)p.cols;
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; t < p.tokens; t += (int64_t)gridDim.x * kTeams) {
+    uint4 y[V], h[V];
+    load_chunks(p.y + t * p.ld_y, c, y);
+    if (p.h) load_chunks(p.h + t * p.ld_h, c, h);
+    float v[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) widen8(y[i], v[i]);
+    if (p.post) {
+      normalise(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
+      with_columns(p.post_weight, c, v, [](float a, float w) { return a * w; });
+    }
+    if (p.gate_kind == DG_GATE_COLUMN) {
+      with_columns(p.gate, c, v, [](float a, float w) { return a * w; });
+    } else if (p.gate_kind == DG_GATE_TOKEN) {
+      const float g = p.gate[t];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= g;
+    }
+    if (p.h) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f[8];
+        widen8(h[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = fmaf(p.res_scale, f[e], v[i][e]);
+      }
+    }
+    if (p.r) store_chunks(p.r + t * p.ld_r, c, v);
+    if (!p.x && !p.q) continue;
+    normalise(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
+    with_columns(p.weight, c, v, [](float a, float w) { return a * w; });
+    with_columns(p.bias, c, v, [](float a, float b) { return a + b; });
+    if (p.x) store_chunks(p.x + t * p.ld_x, c, v);
+    if (!p.q) continue;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      // 16 lanes own a tile; those past the end are whole tiles.
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) m = fmaxf(m, fmaxf(fabsf(v[i][e]), fabsf(v[i][e + 1])));
+      uint32_t u = __float_as_uint(m);  // not negative: ordered like its bits
+      u = umax(u, dpp<kXor1>(u));
+      u = umax(u, dpp<kXor2>(u));
+      u = umax(u, dpp<kHalfMirror>(u));
+      u = umax(u, dpp<kRowMirror>(u));
+      if (!c.in(i)) continue;
+      const float amax = __uint_as_float(u);
+      const int at = c.at(i);
+      const int64_t sf_at = (int64_t)(at / 16) * p.ld_sf + t;
+      uint2 codes;
+      if constexpr (POW2) {
+        const uint32_t e = ue8m0_exponent_f32(amax);
+        const int up = 127 - (int)e;
+        auto q = [&](int j) { return __builtin_ldexpf(v[i][j], up); };
+        codes = make_uint2(e4m3_of4(q(0), q(1), q(2), q(3)), e4m3_of4(q(4), q(5), q(6), q(7)));
+        if (at % 16 == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
+      } else {
+        const TileScale s = tile_scale(amax);
+        codes = make_uint2(codes4<true>(v[i][0], v[i][1], v[i][2], v[i][3], s.s, s.inv),
+                           codes4<true>(v[i][4], v[i][5], v[i][6], v[i][7], s.s, s.inv));
+        if (at % 16 == 0) static_cast<float*>(p.sf)[sf_at] = s.s;
+      }
+      *reinterpret_cast<uint2*>(p.q + t * p.cols + at * 8) = codes;
+    }
+  }
+}
+
+// Gradient.  Each team walks down the rows and keeps the sums over its rows of the
+// column gradients in registers; they leave once, as a row of partial sums of the
+// workgroup.  POST, LAYER: as in the call; EXTRA: whether the gradients of a bias or
+// of a column gate are wanted (registers for two more sums).
+template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
+__global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdParams p) {
+  constexpr int kTeams = kNormThreads<TEAM> / TEAM;
+  __shared__ TeamSums<TEAM> lds;
+  int turn = 0;
+  const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
+  const float inv_cols = 1.0f / (float)p.cols;
+  const bool read_y = POST || p.dgate;
+  float dw[V][8] = {}, db[EXTRA ? V : 1][8] = {}, dpw[POST ? V : 1][8] = {}, dg[EXTRA ? V : 1][8] = {};
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; t < p.tokens; t += (int64_t)gridDim.x * kTeams) {
+    uint4 dx_[V], dr_[V], r_[V], y_[V];
+    if (p.dx) {
+      load_chunks(p.dx + t * p.ld_dx, c, dx_);
+      load_chunks(p.r + t * p.ld_r, c, r_);
+    }
+    if (p.dr) load_chunks(p.dr + t * p.ld_dr, c, dr_);
+    if (read_y) load_chunks(p.y + t * p.ld_y, c, y_);
+    // The sums that both norms' statistics need, together: the mean first (layer),
+    // then squares and products with what is left.
+    float mean_r = 0.0f, mean_y = 0.0f, mean_g = 0.0f;
+    if constexpr (LAYER) {
+      float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float a[8], b[8], w[8];
+        if (p.dx) {
+          widen8(r_[i], a);
+          widen8(dx_[i], b);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+          if (p.weight && c.in(i)) load8(p.weight + c.at(i) * 8, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[0] += a[e], s[2] = fmaf(b[e], w[e], s[2]);
+        }
+        if (POST) {
+          widen8(y_[i], a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[1] += a[e];
+        }
+      }
+      team_sums<TEAM>(s, lds, turn);
+      mean_r = s[0] * inv_cols, mean_y = s[1] * inv_cols, mean_g = s[2] * inv_cols;
+    }
+    float s[3] = {0.0f, 0.0f, 0.0f};  // squares of r, products of g and r, squares of y
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!c.in(i)) continue;
+      float a[8], b[8], w[8];
+      if (p.dx) {
+        widen8(r_[i], a);
+        widen8(dx_[i], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        if (p.weight) load8(p.weight + c.at(i) * 8, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = a[e] - mean_r;
+          s[0] = fmaf(d, d, s[0]);
+          s[1] = fmaf(b[e] * w[e], d, s[1]);
+        }
+      }
+      if (POST) {
+        widen8(y_[i], a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = a[e] - mean_y;
+          s[2] = fmaf(d, d, s[2]);
+        }
+      }
+    }
+    if (p.dx || POST) team_sums<TEAM>(s, lds, turn);
+    const float kr = inverse_root(fmaf(s[0], inv_cols, p.eps));
+    const float ky = POST ? inverse_root(fmaf(s[2], inv_cols, p.eps)) : 1.0f;
+    const float gn = s[1] * inv_cols * kr;  // mean of g n
+    float token_gate = 1.0f;
+    if (p.gate_kind == DG_GATE_TOKEN) token_gate = p.gate[t];
+    float tot[V][8];  // t, then e
+    float after[3] = {0.0f, 0.0f, 0.0f};  // sums of e post_weight, of that times n(y), of t u
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (p.dr) widen8(dr_[i], tot[i]);
+      else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tot[i][e] = 0.0f;
+      }
+      if (!c.in(i)) continue;
+      if (p.dx) {
+        float a[8], b[8], w[8];
+        widen8(r_[i], a);
+        widen8(dx_[i], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+        if (p.weight) load8(p.weight + c.at(i) * 8, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = (a[e] - mean_r) * kr;
+          dw[i][e] = fmaf(b[e], n, dw[i][e]);
+          if constexpr (EXTRA) db[i][e] += b[e];
+          tot[i][e] = fmaf(kr, fmaf(-n, gn, fmaf(b[e], w[e], -mean_g)), tot[i][e]);
+        }
+      }
+      if (p.dh) {
+        float out[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = p.res_scale * tot[i][e];
+        *reinterpret_cast<uint4*>(p.dh + t * p.ld_dh + c.at(i) * 8) = narrow8(out);
+      }
+      float yv[8], pw[8];
+      if (read_y) {
+        widen8(y_[i], yv);
+        if (POST) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pw[e] = 1.0f, yv[e] = (yv[e] - mean_y) * ky;
+          if (p.post_weight) load8(p.post_weight + c.at(i) * 8, pw);
+        }
+        if (p.dgate) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float tu = tot[i][e] * (POST ? yv[e] * pw[e] : yv[e]);
+            if constexpr (EXTRA) dg[i][e] += tu;
+            after[2] += tu;
+          }
+        }
+      }
+      if (p.gate_kind == DG_GATE_COLUMN) {
+        float g[8];
+        load8(p.gate + c.at(i) * 8, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tot[i][e] *= g[e];
+      } else if (p.gate_kind == DG_GATE_TOKEN) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tot[i][e] *= token_gate;
+      }
+      if constexpr (POST) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dpw[i][e] = fmaf(tot[i][e], yv[e], dpw[i][e]);
+          tot[i][e] *= pw[e];
+          after[0] += tot[i][e];
+          after[1] = fmaf(tot[i][e], yv[e], after[1]);
+        }
+      }
+    }
+    if (POST || p.dgate) team_sums<TEAM>(after, lds, turn);
+    if (p.gate_kind == DG_GATE_TOKEN && p.dgate && c.lane == 0) p.dgate[t] = after[2];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!c.in(i)) continue;
+      if constexpr (POST) {
+        float yv[8];
+        widen8(y_[i], yv);
+        const float m = LAYER ? after[0] * inv_cols : 0.0f, mn = after[1] * inv_cols;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tot[i][e] = ky * fmaf(-(yv[e] - mean_y) * ky, mn, tot[i][e] - m);
+      }
+      *reinterpret_cast<uint4*>(p.dy + t * p.ld_dy + c.at(i) * 8) = narrow8(tot[i]);
+    }
+  }
+  // The workgroup's row of partial sums; waves with rows of their own come together
+  // in shared memory, in order.
+  auto leave = [&](float (&sum)[V][8], float* to) {
+    if (!to) return;
+    to += (int64_t)blockIdx.x * p.cols;
+    if constexpr (kTeams > 1) {
+      __shared__ float rows[kTeams][V * TEAM * 8];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rows[threadIdx.x / TEAM][c.at(i) * 8 + e] = sum[i][e];
+      __syncthreads();
+      for (int col = threadIdx.x; col < p.cols; col += kNormThreads<TEAM>) {
+        float all = rows[0][col];
+#pragma unroll
+        for (int k = 1; k < kTeams; ++k) all += rows[k][col];
+        to[col] = all;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!c.in(i)) continue;
+        float4* at = reinterpret_cast<float4*>(to + c.at(i) * 8);
+        at[0] = make_float4(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
+        at[1] = make_float4(sum[i][4], sum[i][5], sum[i][6], sum[i][7]);
+      }
+    }
+  };
+  const int64_t matrix = (int64_t)gridDim.x * p.cols;
+  leave(dw, p.dweight ? p.parts : nullptr);
+  if constexpr (EXTRA) leave(db, p.dbias ? p.parts + matrix : nullptr);
+  if constexpr (POST) leave(dpw, p.dpost_weight ? p.parts + 2 * matrix : nullptr);
+  if constexpr (EXTRA) leave(dg, p.dgate && p.gate_kind == DG_GATE_COLUMN ? p.parts + 3 * matrix : nullptr);
+}
+
+// Workgroup (x, y): 64 columns of matrix y, 16 threads wide (4 columns each) and 16
+// rows tall; the rows' sums come together in shared memory.
+__global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums s) {
+  __shared__ float4 rows[16][16];
+  const float* from = s.from[blockIdx.y];
+  const int at = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int col = blockIdx.x * 64 + at * 4;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < s.cols) {
+#pragma unroll 8
+    for (int k = row; k < s.parts; k += 16) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)k * s.cols + col);
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+  }
+  rows[row][at] = sum;
+  __syncthreads();
+  if (row == 0 && col < s.cols) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) {
+      const float4 v = rows[k][at];
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    *reinterpret_cast<float4*>(s.to[blockIdx.y] + col) = sum;
+  }
+}
+
+template <bool POW2, int TEAM, int V>
+void go_norm(const NormParams& p, hipStream_t stream) {
+  constexpr int kTeams = kNormThreads<TEAM> / TEAM;
+  const int64_t need = ((int64_t)p.tokens + kTeams - 1) / kTeams;
+  const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
+  hipLaunchKernelGGL((norm_kernel<POW2, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
+}
+
+template <bool POW2>
+hipError_t pick_norm(const NormParams& p, hipStream_t stream) {
+  const int chunks = p.cols / 8;
+  if (chunks <= 64) go_norm<POW2, 64, 1>(p, stream);
+  else if (chunks <= 128) go_norm<POW2, 64, 2>(p, stream);
+  else if (chunks <= 256) go_norm<POW2, 256, 1>(p, stream);
+  else if (chunks <= 512) go_norm<POW2, 256, 2>(p, stream);
+  else if (chunks <= 768) go_norm<POW2, 256, 3>(p, stream);
+  else if (chunks <= 1024) go_norm<POW2, 256, 4>(p, stream);
+  else go_norm<POW2, 1024, 2>(p, stream);
+  return hipGetLastError();
+}
+
+constexpr int kMostParts = 256;  // workgroups of the gradient
+
+template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
+void go_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((norm_bwd_kernel<TEAM, V, POST, LAYER, EXTRA>), dim3(norm_bwd_parts(p.tokens, p.cols)),
+                     dim3(kNormThreads<TEAM>), 0, stream, p);
+}
+
+template <int TEAM, int V>
+void pick_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  const bool extra = p.dbias || (p.dgate && p.gate_kind == DG_GATE_COLUMN);
+  auto go = [&](auto post, auto layer) {
+    constexpr bool kPost = decltype(post)::value, kLayer = decltype(layer)::value;
+    if (extra) go_norm_bwd<TEAM, V, kPost, kLayer, true>(p, stream);
+    else go_norm_bwd<TEAM, V, kPost, kLayer, false>(p, stream);
+  };
+  using std::false_type, std::true_type;
+  if (p.post) p.layer ? go(true_type{}, true_type{}) : go(true_type{}, false_type{});
+  else p.layer ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
+}
+
+// Rows that a workgroup of the gradient has at a time.
+int teams_of(int cols) { return cols <= 1024 ? 4 : 1; }
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormParams& p, bool pow2, hipStream_t stream) {
+  return pow2 ? pick_norm<true>(p, stream) : pick_norm<false>(p, stream);
+}
+
+int norm_bwd_parts(int tokens, int cols) {
+  const int64_t need = ((int64_t)tokens + teams_of(cols) - 1) / teams_of(cols);
+  return need < kMostParts ? (int)need : kMostParts;
+}
+
+hipError_t launch_block_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  const int chunks = p.cols / 8;
+  if (p.tokens > 0) {
+    if (chunks <= 64) pick_norm_bwd<64, 1>(p, stream);
+    else if (chunks <= 128) pick_norm_bwd<64, 2>(p, stream);
+    else if (chunks <= 256) pick_norm_bwd<256, 1>(p, stream);
+    else if (chunks <= 512) pick_norm_bwd<256, 2>(p, stream);
+    else if (chunks <= 1024) pick_norm_bwd<512, 2>(p, stream);
+    else pick_norm_bwd<1024, 2>(p, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  ColumnSums s{};
+  s.parts = norm_bwd_parts(p.tokens, p.cols), s.cols = p.cols;
+  const int64_t matrix = (int64_t)s.parts * p.cols;
+  float* column_gate = p.gate_kind == DG_GATE_COLUMN ? p.dgate : nullptr;
+  float* const to[4] = {p.dweight, p.dbias, p.dpost_weight, column_gate};
+  for (int k = 0; k < 4; ++k)
+    if (to[k]) s.from[s.count] = p.parts + k * matrix, s.to[s.count++] = to[k];
+  return s.count ? launch_column_sums(s, stream) : hipSuccess;
+}
+
+hipError_t launch_column_sums(const ColumnSums& c, hipStream_t stream) {
+  hipLaunchKernelGGL(column_sums_kernel, dim3((c.cols + 63) / 64, c.count), dim3(256), 0, stream, c);
+  return hipGetLastError();
+}
+
+}  // namespace dg

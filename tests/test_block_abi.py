@@ -1,0 +1,164 @@
+"""C-ABI checks of the transformer block's operators that need no GPU: every entry
+point include/dg_block.h declares is exported and bound, and arguments that break
+its rules are refused on the host, with a message, before anything is enqueued."""
+
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "dg_block.h")
+
+dg = pytest.importorskip("moe_grouped_gemm_02_amd", reason="libdg.so not built")
+from moe_grouped_gemm_02_amd import block as binding  # noqa: E402
+
+FAKE = 1 << 20  # an aligned non-null address; never dereferenced here
+INVALID, SHAPE, MISALIGNED, WORKSPACE = -1, -2, -3, -4
+
+
+def declarations():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    out = {}
+    for name, args in re.findall(r"(?:int|size_t)\s+(dg_\w+)\s*\(([^)]*)\)\s*;", text):
+        params = [a.strip().rsplit(" ", 1) for a in " ".join(args.split()).split(",")]
+        out[name] = [(t + "*" * n.startswith("*"), n.lstrip("*")) for t, n in params]
+    return out
+
+
+DECLS = declarations()
+
+
+def test_every_declared_entry_point_is_exported_and_bound():
+    out = subprocess.run(["nm", "-D", "--defined-only", dg.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    exported = set(re.findall(r"\bT (dg_[a-z0-9_]+)$", out, flags=re.M))
+    assert set(DECLS) <= exported and set(DECLS) == set(binding.EXPORTED)
+    for name in DECLS:
+        assert callable(getattr(dg, name)) and getattr(dg, name).__module__ == binding.__name__
+        assert len(binding._SIGNATURES[name][1]) == len(DECLS[name])
+
+
+VALID = dict(
+    tokens=64, cols=512, ld_y=512, ld_h=512, ld_r=512, ld_x=512, ld_sf=64, ld_dx=512, ld_dr=512, ld_dy=512, ld_dh=512, kind=0, post=1,
+    gate_kind=1, res_scale=1.0, eps=1e-6, experts=256, topk=8, num_seqs=4, ld_logits=256, ld_add=256, ld_dlogits=256, score=1, coef=1.0,
+    m=64, n=512, k=512, lda=512, ldb=512, ldd=512, ld_sfa=64, ld_res=512, ld_pre=512, ld_dsf=256, act=2, rows=256, ld_dd=512, ld_dsft=512,
+    workspace_bytes=1 << 40, stream=None)
+
+
+def call(name, **kw):
+    args = []
+    for ctype, pname in DECLS[name]:
+        v = kw[pname] if pname in kw else VALID[pname] if pname in VALID else FAKE
+        args.append(ctypes.c_void_p(v) if "*" in ctype else v)
+    return getattr(dg.raw(), name)(*args)
+
+
+NAN = float("nan")
+BAD = [
+    ("dg_block_norm", dict(tokens=-1), INVALID), ("dg_block_norm", dict(cols=0), INVALID), ("dg_block_norm", dict(cols=520), SHAPE),
+    ("dg_block_norm", dict(cols=516, q=0, sf=0), SHAPE), ("dg_block_norm", dict(cols=16512, ld_y=16512), SHAPE),
+    ("dg_block_norm", dict(kind=2), INVALID), ("dg_block_norm", dict(gate_kind=3), INVALID), ("dg_block_norm", dict(gate_kind=-1), INVALID),
+    ("dg_block_norm", dict(gate_kind=0), INVALID), ("dg_block_norm", dict(gate=0), INVALID), ("dg_block_norm", dict(gate=FAKE + 4), MISALIGNED),
+    ("dg_block_norm", dict(gate=FAKE + 2, gate_kind=2), MISALIGNED), ("dg_block_norm", dict(eps=0.0), INVALID),
+    ("dg_block_norm", dict(eps=-1.0), INVALID), ("dg_block_norm", dict(eps=NAN), INVALID), ("dg_block_norm", dict(eps=float("inf")), INVALID),
+    ("dg_block_norm", dict(eps=1e-40), INVALID), ("dg_block_norm", dict(q=0), INVALID), ("dg_block_norm", dict(sf=0), INVALID),
+    ("dg_block_norm", dict(post=0), INVALID), ("dg_block_norm", dict(x=0, q=0, sf=0), INVALID),
+    ("dg_block_norm", dict(x=0, q=0, sf=0, r=0, weight=0, bias=0), INVALID), ("dg_block_norm", dict(ld_y=504), INVALID),
+    ("dg_block_norm", dict(ld_h=516), MISALIGNED), ("dg_block_norm", dict(ld_r=504), INVALID), ("dg_block_norm", dict(ld_x=1 << 60), SHAPE),
+    ("dg_block_norm", dict(ld_sf=60), INVALID), ("dg_block_norm", dict(ld_sf=66), MISALIGNED), ("dg_block_norm", dict(y=0), INVALID),
+    ("dg_block_norm", dict(y=FAKE + 8), MISALIGNED), ("dg_block_norm", dict(weight=FAKE + 4), MISALIGNED),
+    ("dg_block_norm", dict(r=FAKE, h=FAKE, ld_h=520), INVALID), ("dg_block_norm_ue8m0", dict(sf=FAKE + 4), MISALIGNED),
+    ("dg_block_norm_ue8m0", dict(cols=520), SHAPE), ("dg_block_norm_ue8m0", dict(tokens=2**31 - 1, ld_sf=2**31 - 4), INVALID),
+    ("dg_block_norm_bwd", dict(tokens=-1), INVALID), ("dg_block_norm_bwd", dict(cols=16392, ld_dy=16392), SHAPE),
+    ("dg_block_norm_bwd", dict(dx=0), INVALID), ("dg_block_norm_bwd", dict(dx=0, dr=0, weight=0, dweight=0, dbias=0), INVALID),
+    ("dg_block_norm_bwd", dict(dx=0, weight=0, dbias=0), INVALID), ("dg_block_norm_bwd", dict(post=0), INVALID),
+    ("dg_block_norm_bwd", dict(gate=0, gate_kind=0), INVALID), ("dg_block_norm_bwd", dict(dy=0), INVALID),
+    ("dg_block_norm_bwd", dict(r=0), INVALID), ("dg_block_norm_bwd", dict(y=0), INVALID), ("dg_block_norm_bwd", dict(ld_dr=504), INVALID),
+    ("dg_block_norm_bwd", dict(ld_dy=516), MISALIGNED), ("dg_block_norm_bwd", dict(dgate=FAKE + 4), MISALIGNED),
+    ("dg_block_norm_bwd", dict(dweight=FAKE + 8), MISALIGNED), ("dg_block_norm_bwd", dict(workspace_bytes=4 * 16 * 512 * 4 - 1), WORKSPACE),
+    ("dg_block_norm_bwd", dict(workspace=0), WORKSPACE), ("dg_block_norm_bwd", dict(workspace=FAKE + 8), MISALIGNED),
+    ("dg_moe_balance", dict(tokens=-1), INVALID), ("dg_moe_balance", dict(experts=0), INVALID),
+    ("dg_moe_balance", dict(experts=1032, ld_logits=1032), SHAPE), ("dg_moe_balance", dict(topk=0), INVALID),
+    ("dg_moe_balance", dict(topk=33), SHAPE), ("dg_moe_balance", dict(experts=8, topk=9), INVALID), ("dg_moe_balance", dict(num_seqs=0), INVALID),
+    ("dg_moe_balance", dict(seq_offsets=0), INVALID), ("dg_moe_balance", dict(num_seqs=(1 << 20) + 1), SHAPE),
+    ("dg_moe_balance", dict(ld_logits=255), INVALID), ("dg_moe_balance", dict(ld_logits=1 << 60), SHAPE), ("dg_moe_balance", dict(score=2), INVALID),
+    ("dg_moe_balance", dict(tokens=2**31 - 1), SHAPE), ("dg_moe_balance", dict(counts=0), INVALID), ("dg_moe_balance", dict(used=0), INVALID),
+    ("dg_moe_balance", dict(loss=0), INVALID), ("dg_moe_balance", dict(logits=0), INVALID), ("dg_moe_balance", dict(ids=0), INVALID),
+    ("dg_moe_balance", dict(logits=FAKE + 2), MISALIGNED), ("dg_moe_balance_bf16", dict(logits=FAKE + 1), MISALIGNED),
+    ("dg_moe_balance", dict(loss=FAKE + 2), MISALIGNED), ("dg_moe_balance", dict(seq_offsets=FAKE + 2), MISALIGNED),
+    ("dg_moe_balance", dict(workspace=0), WORKSPACE), ("dg_moe_balance", dict(workspace_bytes=64), WORKSPACE),
+    ("dg_moe_balance", dict(workspace=FAKE + 8), MISALIGNED),
+    ("dg_moe_balance_bwd", dict(ld_dlogits=255), INVALID), ("dg_moe_balance_bwd", dict(ld_add=255), INVALID),
+    ("dg_moe_balance_bwd", dict(add=FAKE, dlogits=FAKE, ld_add=260), INVALID), ("dg_moe_balance_bwd", dict(dlogits=0), INVALID),
+    ("dg_moe_balance_bwd", dict(counts=0), INVALID), ("dg_moe_balance_bwd", dict(dloss=FAKE + 2), MISALIGNED),
+    ("dg_moe_balance_bwd_bf16", dict(add=FAKE + 1), MISALIGNED), ("dg_moe_balance_bwd", dict(topk=300), INVALID),
+    ("dg_fp8_gemm_nt_epilogue", dict(act=4), INVALID), ("dg_fp8_gemm_nt_epilogue", dict(act=-1), INVALID),
+    ("dg_fp8_gemm_nt_epilogue", dict(k=500), SHAPE), ("dg_fp8_gemm_nt_epilogue", dict(bias=FAKE + 2), MISALIGNED),
+    ("dg_fp8_gemm_nt_epilogue", dict(residual=FAKE + 8), MISALIGNED), ("dg_fp8_gemm_nt_epilogue", dict(pre=FAKE + 8), MISALIGNED),
+    ("dg_fp8_gemm_nt_epilogue", dict(ld_res=504), INVALID), ("dg_fp8_gemm_nt_epilogue", dict(ld_pre=516), MISALIGNED),
+    ("dg_fp8_gemm_nt_epilogue", dict(ld_pre=1 << 60), SHAPE), ("dg_fp8_gemm_nt_epilogue", dict(dq=0), INVALID),
+    ("dg_fp8_gemm_nt_epilogue", dict(n=520, ldb=512, ldd=520, ld_res=520, ld_pre=520), SHAPE),
+    ("dg_fp8_gemm_nt_epilogue", dict(ld_dsf=60), INVALID), ("dg_fp8_gemm_nt_epilogue", dict(d=0), INVALID),
+    ("dg_fp8_gemm_nt_ue8m0_epilogue", dict(ld_sfa=66), MISALIGNED),
+    ("dg_epilogue_bwd", dict(rows=-1), INVALID), ("dg_epilogue_bwd", dict(cols=500), SHAPE), ("dg_epilogue_bwd", dict(act=9), INVALID),
+    ("dg_epilogue_bwd", dict(rows=2**31 - 1, ld_dsf=2**31), SHAPE), ("dg_epilogue_bwd", dict(cols=1 << 23, ld_dd=1 << 23, ld_pre=1 << 23), SHAPE),
+    ("dg_epilogue_bwd", dict(dqt=0), INVALID), ("dg_epilogue_bwd", dict(dsft=0), INVALID), ("dg_epilogue_bwd", dict(ld_dd=504), INVALID),
+    ("dg_epilogue_bwd", dict(ld_pre=516), MISALIGNED), ("dg_epilogue_bwd", dict(ld_dsf=252), INVALID), ("dg_epilogue_bwd", dict(ld_dsft=508), INVALID),
+    ("dg_epilogue_bwd", dict(pre=0), INVALID), ("dg_epilogue_bwd", dict(dd=0), INVALID), ("dg_epilogue_bwd", dict(dbias=FAKE + 4), MISALIGNED),
+    ("dg_epilogue_bwd", dict(workspace_bytes=2 * 512 * 4 - 1), WORKSPACE), ("dg_epilogue_bwd", dict(workspace=0), WORKSPACE),
+]
+
+
+@pytest.mark.parametrize("name,kw,status", BAD, ids=lambda v: str(v))
+def test_refusals(name, kw, status):
+    assert call(name, **kw) == status
+    assert dg.dg_get_last_error_string() != ""
+
+
+def test_calls_with_nothing_to_do_succeed_without_a_device():
+    assert call("dg_block_norm", tokens=0, gate=0) == 0 and call("dg_block_norm_ue8m0", tokens=0) == 0
+    assert call("dg_block_norm_bwd", tokens=0, dweight=0, dbias=0, dpost_weight=0, dgate=0) == 0
+    assert call("dg_moe_balance_bwd", tokens=0) == 0 and call("dg_moe_balance_bwd_bf16", tokens=0) == 0
+    assert call("dg_fp8_gemm_nt_epilogue", m=0) == 0 and call("dg_fp8_gemm_nt_ue8m0_epilogue", n=0, ldd=512) == 0
+    assert call("dg_epilogue_bwd", rows=0, dbias=0) == 0 and call("dg_epilogue_bwd", cols=0) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the launches would run on fake addresses")
+def test_valid_arguments_reach_the_launch():
+    for name in DECLS:
+        if not name.startswith("dg_get_"):
+            assert call(name) == -5, name
+
+
+def test_workspace_sizes():
+    assert dg.dg_get_block_norm_bwd_workspace_size(0, 512) == 0
+    # four sums for each workgroup, which has four narrow rows at a time or one wide one
+    assert dg.dg_get_block_norm_bwd_workspace_size(64, 512) == 4 * 16 * 512 * 4
+    assert dg.dg_get_block_norm_bwd_workspace_size(64, 2048) == 4 * 64 * 2048 * 4
+    assert dg.dg_get_block_norm_bwd_workspace_size(10, 20000) == 0
+    assert dg.dg_get_moe_balance_workspace_size(-1, 8) == 0 and dg.dg_get_moe_balance_workspace_size(8, 2000) == 0
+    assert dg.dg_get_moe_balance_workspace_size(0, 8) > 0
+    assert dg.dg_get_epilogue_bwd_workspace_size(128, 512) == 0 and dg.dg_get_epilogue_bwd_workspace_size(129, 512) == 2 * 512 * 4
+    # sizes of calls at the end of the range are formed in 64 bits
+    assert dg.dg_get_moe_balance_workspace_size(2**31 - 1, 1024, 1 << 20) > 2**33
+    with pytest.raises(ValueError, match="2\\^31"):
+        dg.dg_get_block_norm_bwd_workspace_size(2**32 + 1, 512)
+
+
+def test_binding_refuses_host_tensors_and_unknown_names():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device tensor"):
+        dg.dg_block_norm(x, x=x)
+    with pytest.raises(TypeError):
+        dg.dg_block_norm(None)
+    with pytest.raises(TypeError):
+        dg.dg_moe_balance(None, None, None, None, None)
+    with pytest.raises(ValueError, match="device tensor"):
+        dg.dg_epilogue_bwd(x, x, x)
+    with pytest.raises(ValueError, match="act"):
+        binding._choice(binding._ACTS, "gelu", "act")
+    with pytest.raises(ValueError, match="kind"):
+        binding._choice(binding._KINDS, None, "kind")
