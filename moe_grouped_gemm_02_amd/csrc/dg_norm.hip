@@ -88,6 +88,11 @@ __device__ __forceinline__ void load_chunks(const uint16_t* row, const Chunks<TE
   for (int i = 0; i < V; ++i) v[i] = c.in(i) ? load_streaming4(row + c.at(i) * 8) : make_uint4(0, 0, 0, 0);
 }
 
+template <bool STREAMING>
+__device__ __forceinline__ void store8(uint16_t* to, const float (&f)[8]) {
+  store<STREAMING>(to, narrow8(f));
+}
+
 template <int TEAM, int V>
 __device__ __forceinline__ void store_chunks(uint16_t* row, const Chunks<TEAM, V>& c, const float (&v)[V][8]) {
 #pragma unroll
@@ -143,6 +148,8 @@ __device__ __forceinline__ void normalise(float (&v)[V][8], const Chunks<TEAM, V
 // Threads of a workgroup: teams smaller than 256 threads share one.
 template <int TEAM>
 constexpr int kNormThreads = TEAM < 256 ? 256 : TEAM;
+template <int TEAM>
+constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 
 template <bool POW2, int TEAM, int V>
 __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) {
@@ -221,27 +228,101 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
   }
 }
 
+// What a thread reads of one row of the gradient.
+template <int V>
+struct NormBwdRaw {
+  uint4 dx[V], dr[V], r[V], y[V];
+};
+
+template <int TEAM, int V>
+__device__ __forceinline__ void load_raw(const NormBwdParams& p, int64_t t, bool read_y, const Chunks<TEAM, V>& c, NormBwdRaw<V>& raw) {
+  if (p.dx) {
+    load_chunks(p.dx + t * p.ld_dx, c, raw.dx);
+    load_chunks(p.r + t * p.ld_r, c, raw.r);
+  }
+  if (p.dr) load_chunks(p.dr + t * p.ld_dr, c, raw.dr);
+  if (read_y) load_chunks(p.y + t * p.ld_y, c, raw.y);
+}
+
+// The parameters' columns (ones without a parameter), where reading them again for
+// each row waits for nothing but itself: loads from memory come back in order, so a
+// row's parameters would wait for the next row, which is on its way (16384 x 7168:
+// GAIN).  In registers, or in shared memory, first and second halves of the chunks
+// apart, so that lanes side by side read 16 bytes side by side; rows of more than 8192
+// values, which are not read ahead, take them from memory.
+enum ColumnsIn { kRegisters, kShared, kMemory };
+template <int TEAM, int V>
+constexpr ColumnsIn kColumnsIn = TEAM * V > 1024 ? kMemory : V == 1 ? kRegisters : kShared;
+template <int TEAM, int V>
+struct ColumnsLds {
+  float4 half[2][kColumnsIn<TEAM, V> == kShared ? V * TEAM : 1];
+};
+template <int TEAM, int V>
+struct Columns {
+  const float* from;
+  const ColumnsLds<TEAM, V>& lds;
+  float kept[8];
+  // The whole workgroup calls it; a barrier follows before the first get().
+  __device__ __forceinline__ Columns(const float* w, ColumnsLds<TEAM, V>& to, const Chunks<TEAM, V>& c) : from(w), lds(to) {
+    if constexpr (kColumnsIn<TEAM, V> == kRegisters) read(c, 0, kept);
+    if constexpr (kColumnsIn<TEAM, V> == kShared) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v[8];
+        read(c, i, v);
+        to.half[0][c.at(i)] = make_float4(v[0], v[1], v[2], v[3]);
+        to.half[1][c.at(i)] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+  }
+  __device__ __forceinline__ void read(const Chunks<TEAM, V>& c, int i, float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+    if (from && c.in(i)) load8(from + c.at(i) * 8, v);
+  }
+  __device__ __forceinline__ void get(const Chunks<TEAM, V>& c, int i, float (&v)[8]) const {
+    if constexpr (kColumnsIn<TEAM, V> == kRegisters) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = kept[e];
+    } else if constexpr (kColumnsIn<TEAM, V> == kShared) {
+      const float4 a = lds.half[0][c.at(i)], b = lds.half[1][c.at(i)];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      read(c, i, v);
+    }
+  }
+};
+
 // Gradient.  Each team walks down the rows and keeps the sums over its rows of the
 // column gradients in registers; they leave once, as a row of partial sums of the
-// workgroup.  POST, LAYER: as in the call; EXTRA: whether the gradients of a bias or
-// of a column gate are wanted (registers for two more sums).
+// workgroup.  The next row is read while this one is worked on.  POST, LAYER: as in
+// the call; EXTRA: whether the gradients of a bias or of a column gate are wanted
+// (registers for two more sums).
 template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
-__global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdParams p) {
-  constexpr int kTeams = kNormThreads<TEAM> / TEAM;
+__global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdParams p) {
+  constexpr int kTeams = kBwdThreads<TEAM> / TEAM;
   __shared__ TeamSums<TEAM> lds;
   int turn = 0;
   const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
   const float inv_cols = 1.0f / (float)p.cols;
   const bool read_y = POST || p.dgate;
+  constexpr bool kAhead = TEAM * V <= 1024;  // 128 registers of 1024 threads do not hold a second row
+  __shared__ ColumnsLds<TEAM, V> columns[3];
+  const Columns<TEAM, V> weight(p.weight, columns[0], c), post_weight(POST ? p.post_weight : nullptr, columns[1], c),
+      gate(p.gate_kind == DG_GATE_COLUMN ? p.gate : nullptr, columns[2], c);
+  __syncthreads();
   float dw[V][8] = {}, db[EXTRA ? V : 1][8] = {}, dpw[POST ? V : 1][8] = {}, dg[EXTRA ? V : 1][8] = {};
-  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; t < p.tokens; t += (int64_t)gridDim.x * kTeams) {
-    uint4 dx_[V], dr_[V], r_[V], y_[V];
-    if (p.dx) {
-      load_chunks(p.dx + t * p.ld_dx, c, dx_);
-      load_chunks(p.r + t * p.ld_r, c, r_);
+  NormBwdRaw<V> raw = {}, next = {};
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  int64_t t = (int64_t)blockIdx.x * kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+  if (kAhead && t < p.tokens) load_raw(p, t, read_y, c, next);
+  for (; t < p.tokens; t += step) {
+    if constexpr (kAhead) {
+      raw = next;
+      if (t + step < p.tokens) load_raw(p, t + step, read_y, c, next);
+    } else {
+      load_raw(p, t, read_y, c, raw);
     }
-    if (p.dr) load_chunks(p.dr + t * p.ld_dr, c, dr_);
-    if (read_y) load_chunks(p.y + t * p.ld_y, c, y_);
     // The sums that both norms' statistics need, together: the mean first (layer),
     // then squares and products with what is left.
     float mean_r = 0.0f, mean_y = 0.0f, mean_g = 0.0f;
@@ -251,16 +332,14 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
       for (int i = 0; i < V; ++i) {
         float a[8], b[8], w[8];
         if (p.dx) {
-          widen8(r_[i], a);
-          widen8(dx_[i], b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-          if (p.weight && c.in(i)) load8(p.weight + c.at(i) * 8, w);
+          widen8(raw.r[i], a);
+          widen8(raw.dx[i], b);
+          weight.get(c, i, w);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[0] += a[e], s[2] = fmaf(b[e], w[e], s[2]);
         }
         if (POST) {
-          widen8(y_[i], a);
+          widen8(raw.y[i], a);
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[1] += a[e];
         }
@@ -274,11 +353,9 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
       if (!c.in(i)) continue;
       float a[8], b[8], w[8];
       if (p.dx) {
-        widen8(r_[i], a);
-        widen8(dx_[i], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-        if (p.weight) load8(p.weight + c.at(i) * 8, w);
+        widen8(raw.r[i], a);
+        widen8(raw.dx[i], b);
+        weight.get(c, i, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = a[e] - mean_r;
@@ -287,7 +364,7 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
         }
       }
       if (POST) {
-        widen8(y_[i], a);
+        widen8(raw.y[i], a);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = a[e] - mean_y;
@@ -299,13 +376,12 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
     const float kr = inverse_root(fmaf(s[0], inv_cols, p.eps));
     const float ky = POST ? inverse_root(fmaf(s[2], inv_cols, p.eps)) : 1.0f;
     const float gn = s[1] * inv_cols * kr;  // mean of g n
-    float token_gate = 1.0f;
-    if (p.gate_kind == DG_GATE_TOKEN) token_gate = p.gate[t];
+    const float token_gate = p.gate_kind == DG_GATE_TOKEN ? p.gate[t] : 1.0f;
     float tot[V][8];  // t, then e
     float after[3] = {0.0f, 0.0f, 0.0f};  // sums of e post_weight, of that times n(y), of t u
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (p.dr) widen8(dr_[i], tot[i]);
+      if (p.dr) widen8(raw.dr[i], tot[i]);
       else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) tot[i][e] = 0.0f;
@@ -313,11 +389,9 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
       if (!c.in(i)) continue;
       if (p.dx) {
         float a[8], b[8], w[8];
-        widen8(r_[i], a);
-        widen8(dx_[i], b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-        if (p.weight) load8(p.weight + c.at(i) * 8, w);
+        widen8(raw.r[i], a);
+        widen8(raw.dx[i], b);
+        weight.get(c, i, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float n = (a[e] - mean_r) * kr;
@@ -330,15 +404,16 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
         float out[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[e] = p.res_scale * tot[i][e];
-        *reinterpret_cast<uint4*>(p.dh + t * p.ld_dh + c.at(i) * 8) = narrow8(out);
+        store8<true>(p.dh + t * p.ld_dh + c.at(i) * 8, out);
       }
-      float yv[8], pw[8];
+      float yv[8], pw[8], g[8];
+      if constexpr (POST) post_weight.get(c, i, pw);
+      gate.get(c, i, g);
       if (read_y) {
-        widen8(y_[i], yv);
+        widen8(raw.y[i], yv);
         if (POST) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) pw[e] = 1.0f, yv[e] = (yv[e] - mean_y) * ky;
-          if (p.post_weight) load8(p.post_weight + c.at(i) * 8, pw);
+          for (int e = 0; e < 8; ++e) yv[e] = (yv[e] - mean_y) * ky;
         }
         if (p.dgate) {
 #pragma unroll
@@ -349,15 +424,8 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
           }
         }
       }
-      if (p.gate_kind == DG_GATE_COLUMN) {
-        float g[8];
-        load8(p.gate + c.at(i) * 8, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tot[i][e] *= g[e];
-      } else if (p.gate_kind == DG_GATE_TOKEN) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tot[i][e] *= token_gate;
-      }
+      for (int e = 0; e < 8; ++e) tot[i][e] *= g[e] * token_gate;
       if constexpr (POST) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -368,19 +436,19 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
         }
       }
     }
-    if (POST || p.dgate) team_sums<TEAM>(after, lds, turn);
+    if (POST || (p.dgate && p.gate_kind == DG_GATE_TOKEN)) team_sums<TEAM>(after, lds, turn);
     if (p.gate_kind == DG_GATE_TOKEN && p.dgate && c.lane == 0) p.dgate[t] = after[2];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!c.in(i)) continue;
       if constexpr (POST) {
         float yv[8];
-        widen8(y_[i], yv);
+        widen8(raw.y[i], yv);
         const float m = LAYER ? after[0] * inv_cols : 0.0f, mn = after[1] * inv_cols;
 #pragma unroll
         for (int e = 0; e < 8; ++e) tot[i][e] = ky * fmaf(-(yv[e] - mean_y) * ky, mn, tot[i][e] - m);
       }
-      *reinterpret_cast<uint4*>(p.dy + t * p.ld_dy + c.at(i) * 8) = narrow8(tot[i]);
+      store8<true>(p.dy + t * p.ld_dy + c.at(i) * 8, tot[i]);
     }
   }
   // The workgroup's row of partial sums; waves with rows of their own come together
@@ -396,7 +464,7 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_bwd_kernel(NormBwdPar
 #pragma unroll
         for (int e = 0; e < 8; ++e) rows[threadIdx.x / TEAM][c.at(i) * 8 + e] = sum[i][e];
       __syncthreads();
-      for (int col = threadIdx.x; col < p.cols; col += kNormThreads<TEAM>) {
+      for (int col = threadIdx.x; col < p.cols; col += kBwdThreads<TEAM>) {
         float all = rows[0][col];
 #pragma unroll
         for (int k = 1; k < kTeams; ++k) all += rows[k][col];
@@ -467,12 +535,11 @@ hipError_t pick_norm(const NormParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-constexpr int kMostParts = 256;  // workgroups of the gradient
 
 template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
 void go_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((norm_bwd_kernel<TEAM, V, POST, LAYER, EXTRA>), dim3(norm_bwd_parts(p.tokens, p.cols)),
-                     dim3(kNormThreads<TEAM>), 0, stream, p);
+                     dim3(kBwdThreads<TEAM>), 0, stream, p);
 }
 
 template <int TEAM, int V>
@@ -488,8 +555,10 @@ void pick_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   else p.layer ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
 }
 
-// Rows that a workgroup of the gradient has at a time.
-int teams_of(int cols) { return cols <= 1024 ? 4 : 1; }
+// Rows that a workgroup of the gradient has at a time, and how many workgroups it
+// takes to fill the card.
+int teams_of(int cols) { return cols <= 1024 ? 8 : 1; }
+int most_parts(int cols) { return cols <= 1024 ? 256 : cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256; }
 
 }  // namespace
 
@@ -499,7 +568,7 @@ hipError_t launch_block_norm(const NormParams& p, bool pow2, hipStream_t stream)
 
 int norm_bwd_parts(int tokens, int cols) {
   const int64_t need = ((int64_t)tokens + teams_of(cols) - 1) / teams_of(cols);
-  return need < kMostParts ? (int)need : kMostParts;
+  return need < most_parts(cols) ? (int)need : most_parts(cols);
 }
 
 hipError_t launch_block_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
@@ -508,7 +577,7 @@ hipError_t launch_block_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
     if (chunks <= 64) pick_norm_bwd<64, 1>(p, stream);
     else if (chunks <= 128) pick_norm_bwd<64, 2>(p, stream);
     else if (chunks <= 256) pick_norm_bwd<256, 1>(p, stream);
-    else if (chunks <= 512) pick_norm_bwd<256, 2>(p, stream);
+    else if (chunks <= 512) pick_norm_bwd<512, 1>(p, stream);
     else if (chunks <= 1024) pick_norm_bwd<512, 2>(p, stream);
     else pick_norm_bwd<1024, 2>(p, stream);
     const hipError_t e = hipGetLastError();
