@@ -70,6 +70,11 @@ __device__ __forceinline__ void store(void* p, uint4 v) {
   if constexpr (STREAMING) store_streaming(p, v);
   else *static_cast<uint4*>(p) = v;
 }
+template <bool STREAMING>
+__device__ __forceinline__ void store(void* p, uint2 v) {
+  if constexpr (STREAMING) store_streaming(p, v);
+  else *static_cast<uint2*>(p) = v;
+}
 // Loads of values that are used once (combine of 32110 rows x 7168: 95 us, against
 // 107.7 with plain loads; requantised transpose 83.6 and 86.5, gated unit's
 // backward 151 and 158).

@@ -93,16 +93,9 @@ __device__ __forceinline__ void store8(uint16_t* to, const float (&f)[8]) {
   store<STREAMING>(to, narrow8(f));
 }
 
+// v = v w with the chunk's columns of w, v without w.
 template <int TEAM, int V>
-__device__ __forceinline__ void store_chunks(uint16_t* row, const Chunks<TEAM, V>& c, const float (&v)[V][8]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (c.in(i)) *reinterpret_cast<uint4*>(row + c.at(i) * 8) = narrow8(v[i]);
-}
-
-// v = f(v, w) with the chunk's columns of w, f(v, 1) without w left out.
-template <int TEAM, int V, typename F>
-__device__ __forceinline__ void with_columns(const float* w, const Chunks<TEAM, V>& c, float (&v)[V][8], F&& f) {
+__device__ __forceinline__ void times_columns(const float* w, const Chunks<TEAM, V>& c, float (&v)[V][8]) {
   if (!w) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -110,15 +103,16 @@ __device__ __forceinline__ void with_columns(const float* w, const Chunks<TEAM, 
     float k[8];
     load8(w + c.at(i) * 8, k);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = f(v[i][e], k[e]);
+    for (int e = 0; e < 8; ++e) v[i][e] *= k[e];
   }
 }
 
-// v = norm(v), without weights.  Layer norms take the mean first and the squares
-// of what is left: a single pass would lose rows with a large mean.
+// What norm(v) multiplies v by; a layer norm's mean is taken off v here.  It takes
+// the mean first and the squares of what is left: a single pass would lose rows with a
+// large mean.
 template <int TEAM, int V>
-__device__ __forceinline__ void normalise(float (&v)[V][8], const Chunks<TEAM, V>& c, bool layer, float inv_cols, float eps,
-                                          TeamSums<TEAM>& lds, int& turn) {
+__device__ __forceinline__ float norm_scale(float (&v)[V][8], const Chunks<TEAM, V>& c, bool layer, float inv_cols, float eps,
+                                            TeamSums<TEAM>& lds, int& turn) {
   if (layer) {
     float sum[1] = {0.0f};
 #pragma unroll
@@ -138,11 +132,38 @@ __device__ __forceinline__ void normalise(float (&v)[V][8], const Chunks<TEAM, V
 #pragma unroll
     for (int e = 0; e < 8; ++e) squares[0] = fmaf(v[i][e], v[i][e], squares[0]);
   team_sums<TEAM>(squares, lds, turn);
-  const float k = inverse_root(fmaf(squares[0], inv_cols, eps));
+  return inverse_root(fmaf(squares[0], inv_cols, eps));
+}
+
+// Codes of 8 values x + rest (rest: what the rounding of x left), a tile of 128 by 16
+// lanes.  The quotient takes in both residuals, so that a code differs from that of the
+// exact value only where that lies within a rounding of a boundary (4096 x 7168, of 29M
+// codes: GAIN).
+template <bool POW2>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], const float (&rest)[8], float& s, uint32_t& e) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] *= k;
+  for (int i = 0; i < 8; i += 2) m = fmaxf(m, fmaxf(fabsf(x[i] + rest[i]), fabsf(x[i + 1] + rest[i + 1])));
+  uint32_t u = __float_as_uint(m);  // not negative: ordered like its bits
+  u = umax(u, dpp<kXor1>(u));
+  u = umax(u, dpp<kXor2>(u));
+  u = umax(u, dpp<kHalfMirror>(u));
+  u = umax(u, dpp<kRowMirror>(u));
+  const float amax = __uint_as_float(u);
+  if constexpr (POW2) {
+    e = ue8m0_exponent_f32(amax);
+    const int up = 127 - (int)e;
+    auto q = [&](int j) { return __builtin_ldexpf(x[j] + rest[j], up); };
+    return make_uint2(e4m3_of4(q(0), q(1), q(2), q(3)), e4m3_of4(q(4), q(5), q(6), q(7)));
+  } else {
+    const TileScale t = tile_scale(amax);
+    s = t.s;
+    auto q = [&](int j) {
+      const float p = x[j] * t.inv;
+      return fmaf(fmaf(-t.s, p, x[j]) + rest[j], t.inv, p);
+    };
+    return make_uint2(e4m3_of4(q(0), q(1), q(2), q(3)), e4m3_of4(q(4), q(5), q(6), q(7)));
+  }
 }
 
 // Threads of a workgroup: teams smaller than 256 threads share one.
@@ -151,7 +172,10 @@ constexpr int kNormThreads = TEAM < 256 ? 256 : TEAM;
 template <int TEAM>
 constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 
-template <bool POW2, int TEAM, int V>
+// STREAMING: results larger than the L2s, which nothing reads back through them
+// (store_streaming; 4096 x 7168 with r, bf16 rows and codes: 49.0 us, and 54.5 with
+// plain stores).
+template <bool POW2, bool STREAMING, int TEAM, int V>
 __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) {
   constexpr int kTeams = kNormThreads<TEAM> / TEAM;
   static_assert(kTeams == 1 || TEAM == 64, "teams that share a workgroup are waves");
@@ -159,7 +183,8 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
   int turn = 0;
   const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
   const float inv_cols = 1.0f / (float)p.cols;
-  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; t < p.tokens; t += (int64_t)gridDim.x * kTeams) {
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM); t < p.tokens; t += step) {
     uint4 y[V], h[V];
     load_chunks(p.y + t * p.ld_y, c, y);
     if (p.h) load_chunks(p.h + t * p.ld_h, c, h);
@@ -167,11 +192,15 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
 #pragma unroll
     for (int i = 0; i < V; ++i) widen8(y[i], v[i]);
     if (p.post) {
-      normalise(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
-      with_columns(p.post_weight, c, v, [](float a, float w) { return a * w; });
+      const float k = norm_scale(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= k;
+      times_columns(p.post_weight, c, v);
     }
     if (p.gate_kind == DG_GATE_COLUMN) {
-      with_columns(p.gate, c, v, [](float a, float w) { return a * w; });
+      times_columns(p.gate, c, v);
     } else if (p.gate_kind == DG_GATE_TOKEN) {
       const float g = p.gate[t];
 #pragma unroll
@@ -188,42 +217,53 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
         for (int e = 0; e < 8; ++e) v[i][e] = fmaf(p.res_scale, f[e], v[i][e]);
       }
     }
-    if (p.r) store_chunks(p.r + t * p.ld_r, c, v);
+    if (p.r) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (c.in(i)) store8<STREAMING>(p.r + t * p.ld_r + c.at(i) * 8, v[i]);
+    }
     if (!p.x && !p.q) continue;
-    normalise(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
-    with_columns(p.weight, c, v, [](float a, float w) { return a * w; });
-    with_columns(p.bias, c, v, [](float a, float b) { return a + b; });
-    if (p.x) store_chunks(p.x + t * p.ld_x, c, v);
-    if (!p.q) continue;
+    const float k = norm_scale(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      // 16 lanes own a tile; those past the end are whole tiles.
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) m = fmaxf(m, fmaxf(fabsf(v[i][e]), fabsf(v[i][e + 1])));
-      uint32_t u = __float_as_uint(m);  // not negative: ordered like its bits
-      u = umax(u, dpp<kXor1>(u));
-      u = umax(u, dpp<kXor2>(u));
-      u = umax(u, dpp<kHalfMirror>(u));
-      u = umax(u, dpp<kRowMirror>(u));
-      if (!c.in(i)) continue;
-      const float amax = __uint_as_float(u);
       const int at = c.at(i);
-      const int64_t sf_at = (int64_t)(at / 16) * p.ld_sf + t;
-      uint2 codes;
-      if constexpr (POW2) {
-        const uint32_t e = ue8m0_exponent_f32(amax);
-        const int up = 127 - (int)e;
-        auto q = [&](int j) { return __builtin_ldexpf(v[i][j], up); };
-        codes = make_uint2(e4m3_of4(q(0), q(1), q(2), q(3)), e4m3_of4(q(4), q(5), q(6), q(7)));
-        if (at % 16 == 0) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)e;
+      float w[8], x[8], rest[8];
+      if (p.weight && c.in(i)) {
+        load8(p.weight + at * 8, w);
       } else {
-        const TileScale s = tile_scale(amax);
-        codes = make_uint2(codes4<true>(v[i][0], v[i][1], v[i][2], v[i][3], s.s, s.inv),
-                           codes4<true>(v[i][4], v[i][5], v[i][6], v[i][7], s.s, s.inv));
-        if (at % 16 == 0) static_cast<float*>(p.sf)[sf_at] = s.s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
       }
-      *reinterpret_cast<uint2*>(p.q + t * p.cols + at * 8) = codes;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = v[i][e] * k;
+        x[e] = n * w[e];
+        rest[e] = fmaf(fmaf(v[i][e], k, -n), w[e], fmaf(n, w[e], -x[e]));
+      }
+      if (p.bias && c.in(i)) {
+        float b[8];
+        load8(p.bias + at * 8, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // x + b = sum + what its rounding leaves (exact in float32, whichever is larger)
+          const float sum = x[e] + b[e], of_b = sum - x[e];
+          rest[e] += (x[e] - (sum - of_b)) + (b[e] - of_b);
+          x[e] = sum;
+        }
+      }
+      if (p.x && c.in(i)) store8<STREAMING>(p.x + t * p.ld_x + at * 8, x);
+      if (!p.q) continue;
+      // 16 lanes own a tile; those past the row's end are whole tiles.
+      float s;
+      uint32_t exponent;
+      const uint2 codes = encode8<POW2>(x, rest, s, exponent);
+      if (!c.in(i)) continue;
+      store<STREAMING>(p.q + t * p.cols + at * 8, codes);
+      if (at % 16 == 0) {
+        const int64_t sf_at = (int64_t)(at / 16) * p.ld_sf + t;
+        if constexpr (POW2) static_cast<uint8_t*>(p.sf)[sf_at] = (uint8_t)exponent;
+        else static_cast<float*>(p.sf)[sf_at] = s;
+      }
     }
   }
 }
@@ -514,27 +554,24 @@ __global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums s) {
   }
 }
 
-template <bool POW2, int TEAM, int V>
+template <bool POW2, bool STREAMING, int TEAM, int V>
 void go_norm(const NormParams& p, hipStream_t stream) {
   constexpr int kTeams = kNormThreads<TEAM> / TEAM;
   const int64_t need = ((int64_t)p.tokens + kTeams - 1) / kTeams;
   const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
-  hipLaunchKernelGGL((norm_kernel<POW2, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
+  hipLaunchKernelGGL((norm_kernel<POW2, STREAMING, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
 }
 
-template <bool POW2>
-hipError_t pick_norm(const NormParams& p, hipStream_t stream) {
+template <bool POW2, bool STREAMING>
+void pick_norm(const NormParams& p, hipStream_t stream) {
   const int chunks = p.cols / 8;
-  if (chunks <= 64) go_norm<POW2, 64, 1>(p, stream);
-  else if (chunks <= 128) go_norm<POW2, 64, 2>(p, stream);
-  else if (chunks <= 256) go_norm<POW2, 256, 1>(p, stream);
-  else if (chunks <= 512) go_norm<POW2, 256, 2>(p, stream);
-  else if (chunks <= 768) go_norm<POW2, 256, 3>(p, stream);
-  else if (chunks <= 1024) go_norm<POW2, 256, 4>(p, stream);
-  else go_norm<POW2, 1024, 2>(p, stream);
-  return hipGetLastError();
+  if (chunks <= 64) go_norm<POW2, STREAMING, 64, 1>(p, stream);
+  else if (chunks <= 128) go_norm<POW2, STREAMING, 64, 2>(p, stream);
+  else if (chunks <= 256) go_norm<POW2, STREAMING, 256, 1>(p, stream);
+  else if (chunks <= 512) go_norm<POW2, STREAMING, 256, 2>(p, stream);
+  else if (chunks <= 1024) go_norm<POW2, STREAMING, 512, 2>(p, stream);
+  else go_norm<POW2, STREAMING, 1024, 2>(p, stream);
 }
-
 
 template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
 void go_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
@@ -563,7 +600,10 @@ int most_parts(int cols) { return cols <= 1024 ? 256 : cols <= 2048 ? 1024 : col
 }  // namespace
 
 hipError_t launch_block_norm(const NormParams& p, bool pow2, hipStream_t stream) {
-  return pow2 ? pick_norm<true>(p, stream) : pick_norm<false>(p, stream);
+  const bool streaming = (int64_t)p.tokens * p.cols > (int64_t)8 << 20;
+  if (pow2) streaming ? pick_norm<true, true>(p, stream) : pick_norm<true, false>(p, stream);
+  else streaming ? pick_norm<false, true>(p, stream) : pick_norm<false, false>(p, stream);
+  return hipGetLastError();
 }
 
 int norm_bwd_parts(int tokens, int cols) {
