@@ -16,8 +16,6 @@
 namespace dg {
 namespace {
 
-constexpr int kWaves = 4;
-
 // Sequence ends, brought into [0, tokens].
 struct Sequences {
   const int32_t* offsets;
@@ -26,35 +24,43 @@ struct Sequences {
     if (!offsets) return s == 0 ? 0 : tokens;
     return min(max(offsets[s], 0), tokens);
   }
-  // The first sequence that ends behind token t (count: none).
-  __device__ __forceinline__ int of(int t) const {
+  // The first sequence that ends behind token t (count: none): the wave looks at 64
+  // places at a time, each the last of an equal part of what is left.
+  __device__ __forceinline__ int of(int t, int lane) const {
     int lo = 0, hi = count;
     while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (at(mid + 1) > t) hi = mid;
-      else lo = mid + 1;
+      const int part = (hi - lo + 63) / 64;
+      const int last = (int)min((int64_t)lo + (int64_t)(lane + 1) * part, (int64_t)hi) - 1;
+      const uint64_t behind = __ballot(at(last + 1) > t);
+      if (behind == 0) return hi;
+      const int k = __builtin_ctzll(behind);
+      hi = (int)lane_value((uint32_t)last, k);
+      lo += k * part;
     }
-    return lo;
+    return hi;
   }
 };
 
-// f(s, from, to) for each sequence s with tokens in [t0, t1), and those; uniform.
-// `from` grows with every turn whatever the offsets hold: the sequence that is
-// found ends behind it.
+// f(s, from, to) for each sequence s with tokens in [t0, t1), and those; the same in
+// every wave.  A wave holds the ends of 64 sequences at a time, so that the step from
+// one sequence to the next reads no memory.  t grows with every turn whatever the
+// offsets hold: the sequence that is found or taken ends behind it.
 template <typename F>
-__device__ __forceinline__ void for_sequences(const Sequences& q, int t0, int t1, F&& f) {
+__device__ __forceinline__ void for_sequences(const Sequences& q, int t0, int t1, int lane, F&& f) {
   int t = t0;
-  while (t < t1) {
-    const int s = q.of(t);
-    if (s >= q.count) return;
-    const int begin = q.at(s);
-    if (begin > t) {
-      t = begin;
-      continue;
+  for (int first = q.of(t, lane); first < q.count; first = q.of(t, lane)) {
+    const int s = first + lane;
+    const int end = s < q.count ? q.at(s + 1) : -1;
+    t = max(t, q.at(first));
+    while (t < t1) {
+      const uint64_t behind = __ballot(end > t);
+      if (behind == 0) break;
+      const int k = __builtin_ctzll(behind);
+      const int to = min((int)lane_value((uint32_t)end, k), t1);
+      f(first + k, t, to);
+      t = to;
     }
-    const int end = min(q.at(s + 1), t1);
-    f(s, t, end);
-    t = end;
+    if (t >= t1) return;
   }
 }
 
@@ -99,25 +105,38 @@ __device__ __forceinline__ bool shares(const float (&x)[V], float (&p)[V], float
   return __ballot(open) != 0;
 }
 
+// Workgroup: a chunk of tokens, its waves one token after another, the next one read
+// ahead.  WAVES: 16 (chunks of 16 tokens and more, at most 512 of them up to 128K
+// tokens: few rows for the second launch to add; 32768 x 256: GAIN).
+constexpr int kSumWaves = 16, kMostChunks = 256;
+
 template <bool VEC, typename T, int V>
-__global__ __launch_bounds__(64 * kWaves) void balance_kernel(BalanceParams p) {
-  __shared__ float sums[kWaves][64 * V];
+__global__ __launch_bounds__(64 * kSumWaves) void balance_kernel(BalanceParams p) {
+  __shared__ float sums[kSumWaves][64 * V];
   __shared__ int counts[64 * V];
-  __shared__ int used[kWaves];
+  __shared__ int used[kSumWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0;
   const Sequences seqs = {p.offsets, p.seqs, p.tokens};
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = t0 + p.chunk;
-  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), [&](int s, int from, int to) {
-    for (int e = threadIdx.x; e < p.experts; e += 64 * kWaves) counts[e] = 0;
+  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), lane, [&](int s, int from, int to) {
+    for (int e = threadIdx.x; e < p.experts; e += 64 * kSumWaves) counts[e] = 0;
+    float sum[V] = {}, next[V];
+    int here = 0, next_id = -1;
+    auto fetch = [&](int t) {
+      fetch_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, next);
+      if (lane < p.topk) next_id = p.ids[(int64_t)t * p.topk + lane];
+    };
+    if (from + wave < to) fetch(from + wave);
     __syncthreads();
-    float sum[V] = {};
-    int here = 0;
-    for (int t = from + wave; t < to; t += kWaves) {
+    for (int t = from + wave; t < to; t += kSumWaves) {
       float x[V], share[V], rest[V];
-      load_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, sums[wave], x);
-      const int id = lane < p.topk ? p.ids[(int64_t)t * p.topk + lane] : -1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = next[i];
+      const int id = next_id;
+      if (t + kSumWaves < to) fetch(t + kSumWaves);
+      arrange_row<VEC>(lane, sums[wave], x);
       if (!shares<V>(x, share, rest, p.sigmoid != 0)) continue;
       ++here;
       if (id >= 0 && id < p.experts) atomicAdd(&counts[id], 1);
@@ -130,11 +149,19 @@ __global__ __launch_bounds__(64 * kWaves) void balance_kernel(BalanceParams p) {
     if (lane == 0) used[wave] = here;
     __syncthreads();
     const int64_t row = (int64_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < p.experts; e += 64 * kWaves) {
-      p.share_parts[row * p.experts + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+    for (int e = threadIdx.x; e < p.experts; e += 64 * kSumWaves) {
+      float all = sums[0][e];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) all += sums[w][e];
+      p.share_parts[row * p.experts + e] = all;
       p.count_parts[row * p.experts + e] = counts[e];
     }
-    if (threadIdx.x == 0) p.used_parts[row] = used[0] + used[1] + used[2] + used[3];
+    if (threadIdx.x == 0) {
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < kSumWaves; ++w) all += used[w];
+      p.used_parts[row] = all;
+    }
     __syncthreads();
   });
 }
@@ -203,7 +230,7 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
   }
 }
 
-constexpr int kBwdChunk = 16;  // tokens of a workgroup
+constexpr int kWaves = 4, kBwdChunk = 16;  // waves and tokens of a workgroup
 
 template <bool VEC, typename T, int V>
 __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams p) {
@@ -214,7 +241,7 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams 
   const float dloss = p.dloss ? *p.dloss : 1.0f;
   const int64_t t0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kBwdChunk, t1 = t0 + kBwdChunk;
   if (t0 >= p.tokens) return;
-  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), [&](int s, int from, int to) {
+  for_sequences(seqs, (int)t0, (int)(t1 < p.tokens ? t1 : p.tokens), lane, [&](int s, int from, int to) {
     const int used = p.used[s];
     const float n = (float)used;
     const float a = used > 0 ? dloss * p.coef / ((float)p.seqs * n) : 0.0f;
@@ -263,13 +290,13 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams 
 
 template <bool VEC, typename T, int V>
 void go(const BalanceParams& p, bool bwd, hipStream_t stream) {
-  const dim3 block(64 * kWaves);
   if (bwd) {
     const GridXY grid = spread(((int64_t)p.tokens + kBwdChunk - 1) / kBwdChunk);
-    hipLaunchKernelGGL((balance_bwd_kernel<VEC, T, V>), dim3(grid.x, grid.y), block, 0, stream, p);
+    hipLaunchKernelGGL((balance_bwd_kernel<VEC, T, V>), dim3(grid.x, grid.y), dim3(64 * kWaves), 0, stream, p);
   } else {
     const int64_t chunks = ((int64_t)p.tokens + p.chunk - 1) / p.chunk;
-    hipLaunchKernelGGL((balance_kernel<VEC, T, V>), dim3((unsigned)(chunks > 0 ? chunks : 1)), block, 0, stream, p);
+    hipLaunchKernelGGL((balance_kernel<VEC, T, V>), dim3((unsigned)(chunks > 0 ? chunks : 1)), dim3(64 * kSumWaves),
+                       0, stream, p);
   }
 }
 
@@ -299,9 +326,8 @@ void pick(const BalanceParams& p, bool bwd, hipStream_t stream) {
 }  // namespace
 
 int balance_chunk(int tokens) {
-  // At most 65536 chunks.
-  const int64_t least = ((int64_t)tokens + 65535) / 65536;
-  return (int)(least > 32 ? least : 32);
+  const int64_t share = ((int64_t)tokens + kMostChunks - 1) / kMostChunks;
+  return share <= kSumWaves ? kSumWaves : (int)((share + kSumWaves - 1) / kSumWaves * kSumWaves);
 }
 
 int64_t balance_slots(int tokens, int seqs) {

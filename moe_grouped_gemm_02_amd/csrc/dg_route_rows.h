@@ -23,11 +23,12 @@ struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
 // The lane's V logits, -inf past the last expert.  VEC: rows and their length
 // allow whole vectors (decided on the host); otherwise the wave reads them in
 // order and hands them out through its 64 V words of shared memory (32768 rows of
-// 500: 41 us, 60 with each lane reading its own).
+// 500: 41 us, 60 with each lane reading its own).  The two steps apart, for rows that
+// are read ahead: fetch_row, and arrange_row on what it read.
 template <bool VEC, typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int experts, int lane, float* lds, float (&x)[V]) {
-  const int e0 = lane * V;
+__device__ __forceinline__ void fetch_row(const T* row, int experts, int lane, float (&x)[V]) {
   if constexpr (VEC) {
+    const int e0 = lane * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = -INFINITY;
     if (e0 < experts) {
@@ -35,21 +36,29 @@ __device__ __forceinline__ void load_row(const T* row, int experts, int lane, fl
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = widen(in.v[i]);
     }
-  } else if constexpr (V == 1) {
-    x[0] = lane < experts ? widen(row[lane]) : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = i * 64 + lane;
       x[i] = e < experts ? widen(row[e]) : -INFINITY;
     }
+  }
+}
+template <bool VEC, int V>
+__device__ __forceinline__ void arrange_row(int lane, float* lds, float (&x)[V]) {
+  if constexpr (!VEC && V > 1) {
     wave_fence();
 #pragma unroll
     for (int i = 0; i < V; ++i) lds[i * 64 + lane] = x[i];
     wave_fence();
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = lds[e0 + i];
+    for (int i = 0; i < V; ++i) x[i] = lds[lane * V + i];
   }
+}
+template <bool VEC, typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int experts, int lane, float* lds, float (&x)[V]) {
+  fetch_row<VEC>(row, experts, lane, x);
+  arrange_row<VEC>(lane, lds, x);
 }
 
 // s = 1 / (1 + e^-x) and 1 - s, each with its own relative accuracy: the smaller
