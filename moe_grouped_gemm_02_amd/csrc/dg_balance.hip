@@ -106,8 +106,10 @@ __device__ __forceinline__ bool shares(const float (&x)[V], float (&p)[V], float
 }
 
 // Workgroup: a chunk of tokens, its waves one token after another, the next one read
-// ahead.  WAVES: 16 (chunks of 16 tokens and more, at most 512 of them up to 128K
-// tokens: few rows for the second launch to add; 32768 x 256: GAIN).
+// ahead (four ahead measure the same, and take registers).  At most 256 chunks: few rows
+// for the second launch to add (32768 x 256: 13.4 us here and 6.5 there, against 13.2
+// and 12.6 with 1024 chunks of 4 waves), one workgroup a CU, which reads its 131 KB at
+// what a CU reaches.
 constexpr int kSumWaves = 16, kMostChunks = 256;
 
 template <bool VEC, typename T, int V>
@@ -212,8 +214,10 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
     const float sum = wave_sum(product);
     if (at == 0) {
       __hip_atomic_store(&p.loss_parts[(int64_t)s * gridDim.y + blockIdx.y], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __threadfence();
-      last = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
+      // The store goes past the L2 and is waited for, like the reads below: no cache as a
+      // whole has to be written back or dropped (8191 x 72: 7.2 -> 5.9 us).
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+      last = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x * gridDim.y - 1;
     }
   }
   __syncthreads();
