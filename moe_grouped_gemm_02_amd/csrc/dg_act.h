@@ -21,12 +21,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 // (1 + tanh(u)) / 2 is the sigmoid of 2 u, which keeps its relative accuracy
 // for negative z.
 constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.071354816272600247f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
+// Values that are rounded to bf16 next: z / (1 + 2^-u) with the hardware's 2^x and
+// reciprocal, within 2^-22 and |u| 2^-23 of themselves; no range is cut, since 2^-u may
+// become infinite or 0 (4096 x 4096 x 7168 with GELU: GAIN).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
+  auto gated = [](float v, float u) { return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u)); };
   if constexpr (ACT == DG_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  else if constexpr (ACT == DG_ACT_SILU) return z * sigmoid(z).sig;
-  else if constexpr (ACT == DG_ACT_GELU_TANH) return z * sigmoid(z * fmaf(kGelu3, z * z, kGelu1)).sig;
+  else if constexpr (ACT == DG_ACT_SILU) return gated(z, z * kLog2e);
+  else if constexpr (ACT == DG_ACT_GELU_TANH) return gated(z, z * fmaf(kGelu3 * kLog2e, z * z, kGelu1 * kLog2e));
   else return z;
 }
 

@@ -335,53 +335,73 @@ __device__ __forceinline__ const float* scale_ptr(const float* base, int64_t off
   return base + offset;
 }
 
-// z = sum + bias, z kept as bf16, act(z) + residual, on the wave's sums before
-// they are rounded: the lane's row of fragment i is row0 + 16 i, its columns of
-// fragment j col0 + 16 j .. + 3.  The K loop's registers are dead here; bias is
-// read once for all rows, the residual one fragment row at a time.
+// What an epilogue adds to the wave's sums: the lane's row of fragment i is
+// row0 + 16 i, its columns of fragment j col0 + 16 j .. + 3.  Tiles of up to 8
+// fragments a wave read all of it before their K loop, which hides the wait (128 x 7168 x
+// 16384 with bias and residual: 43.9 -> 41.5 us), those of up to 20 at once behind it
+// (4096 x 2112 x 7168 with all terms: 90.5 us, 96.9 a row ahead).  The 256 x 256 tile's
+// 32 fragments leave registers for two rows of the residual, which is read a row ahead
+// (4096 x 4096 x 7168 with UE8M0 scales and all terms: 121 us, 126 at once).
 template <class T>
-__device__ __forceinline__ void apply_epilogue(const GemmEpilogue& e, v4f (&acc)[T::FM][T::FN], int row0, int col0,
-                                               int m, int n) {
-  // Four bf16 values at col, or as many as the matrix has.
-  auto load4 = [&](const uint16_t* at, int col) -> uint2 {
-    if (col + 3 < n) return *reinterpret_cast<const uint2*>(at + col);
-    uint32_t v[3] = {0, 0, 0};
-#pragma unroll
-    for (int c = 0; c < 3; ++c)
-      if (col + c < n) v[c] = at[col + c];
-    return make_uint2(v[0] | (v[1] << 16), v[2]);
-  };
-  if (e.bias) {
+struct EpilogueTerms {
+  static constexpr bool kEarly = T::FM * T::FN <= 8, kWhole = T::FM * T::FN <= 20;
+  float bias[T::FN][4];
+  uint2 residual[kWhole ? T::FM : 2][T::FN];
+  // Four bf16 values of fragment row i, or as many as the matrix has.
+  __device__ __forceinline__ void load_row(const GemmEpilogue& e, int i, int row0, int col0, int m, int n) {
+    if (!kWhole && !e.residual) return;
+    const int row = row0 + 16 * i;
+    const uint16_t* from = e.residual + (int64_t)row * e.ld_res;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
       const int col = col0 + 16 * j;
-      float b[4];
+      uint2& to = residual[kWhole ? i : i & 1][j];
+      to = make_uint2(0, 0);
+      if (!e.residual || row >= m) continue;
+      if (col + 3 < n) {
+        to = *reinterpret_cast<const uint2*>(from + col);
+      } else {
+        uint32_t v[3] = {0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) b[c] = col + c < n ? e.bias[col + c] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][j][c] += b[c];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < T::FM; ++i) {
-    const int row = row0 + 16 * i;
-    const bool in = row < m;
-    uint2 res[T::FN];
-    if (e.residual) {
-#pragma unroll
-      for (int j = 0; j < T::FN; ++j) {
-        res[j] = make_uint2(0, 0);
-        if (in) res[j] = load4(e.residual + (int64_t)row * e.ld_res, col0 + 16 * j);
+        for (int c = 0; c < 3; ++c)
+          if (col + c < n) v[c] = from[col + c];
+        to = make_uint2(v[0] | (v[1] << 16), v[2]);
       }
     }
-    if (e.pre && in) {
-      uint16_t* to = e.pre + (int64_t)row * e.ld_pre;
+  }
+  __device__ __forceinline__ void load(const GemmEpilogue& e, int row0, int col0, int m, int n) {
+#pragma unroll
+    for (int i = 0; i < (kWhole ? T::FM : 1); ++i) load_row(e, i, row0, col0, m, n);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = col0 + 16 * j + c;
+        bias[j][c] = e.bias && col < n ? e.bias[col] : 0.0f;
+      }
+  }
+};
+
+// z = sum + bias, z kept as bf16, act(z) + residual, on the wave's sums.  Those of the
+// 256 x 256 tile leave rounded and paired up, a fragment row at a time.
+template <class T>
+__device__ __forceinline__ void apply_epilogue(const GemmEpilogue& e, EpilogueTerms<T>& terms, v4f (&acc)[T::FM][T::FN],
+                                               uint32_t (&packed)[T::FM][T::FN][2], int row0, int col0, int m, int n) {
+  static_for<T::FM>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    if constexpr (!EpilogueTerms<T>::kWhole && i + 1 < T::FM) terms.load_row(e, i + 1, row0, col0, m, n);
+    const uint2(&res)[T::FN] = terms.residual[EpilogueTerms<T>::kWhole ? i : i & 1];
+    float z[T::FN][4];
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[j][c] = acc[i][j][c] + terms.bias[j][c];
+    if (e.pre && row0 + 16 * i < m) {
+      uint16_t* to = e.pre + (int64_t)(row0 + 16 * i) * e.ld_pre;
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) {
         const int col = col0 + 16 * j;
-        const uint32_t lo = bf16_pair(acc[i][j][0], acc[i][j][1]), hi = bf16_pair(acc[i][j][2], acc[i][j][3]);
+        const uint32_t lo = bf16_pair(z[j][0], z[j][1]), hi = bf16_pair(z[j][2], z[j][3]);
         if (col + 3 < n) {
           *reinterpret_cast<uint2*>(to + col) = make_uint2(lo, hi);
         } else {
@@ -395,18 +415,28 @@ __device__ __forceinline__ void apply_epilogue(const GemmEpilogue& e, v4f (&acc)
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][j][c] = act_value<decltype(act)::value>(acc[i][j][c]);
+        for (int c = 0; c < 4; ++c) z[j][c] = act_value<decltype(act)::value>(z[j][c]);
     });
-    if (e.residual) {
+    // (A branch here costs the 256 x 160 tile 70 spilled registers: zeros are added.)
+    if (EpilogueTerms<T>::kWhole || e.residual) {
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) {
-        acc[i][j][0] += __uint_as_float(res[j].x << 16);
-        acc[i][j][1] += __uint_as_float(res[j].x & 0xFFFF0000u);
-        acc[i][j][2] += __uint_as_float(res[j].y << 16);
-        acc[i][j][3] += __uint_as_float(res[j].y & 0xFFFF0000u);
+        z[j][0] += __uint_as_float(res[j].x << 16);
+        z[j][1] += __uint_as_float(res[j].x & 0xFFFF0000u);
+        z[j][2] += __uint_as_float(res[j].y << 16);
+        z[j][3] += __uint_as_float(res[j].y & 0xFFFF0000u);
       }
     }
-  }
+    if constexpr (EpilogueTerms<T>::kWhole) {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) acc[i][j] = v4f{z[j][0], z[j][1], z[j][2], z[j][3]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j) packed[i][j][0] = bf16_pair(z[j][0], z[j][1]), packed[i][j][1] = bf16_pair(z[j][2], z[j][3]);
+      // Without this the compiler reads every row's residual first and spills.
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  });
 }
 
 // SF: kScaleF32 (fp32 scales, promoted on the VALU) or kScaleUE8M0 (power-of-
@@ -747,6 +777,13 @@ __global__ __launch_bounds__(T::kThreads) void gemm_kernel(GemmParams p, Schedul
           if constexpr (j * T::kSpreadRows / DP::kIssue == i) issue_piece(kb, buf, jc);
         });
       };
+
+      constexpr bool kEpilogue = std::is_same_v<EPI, GemmEpilogue>;
+      std::conditional_t<kEpilogue, EpilogueTerms<T>, NoEpilogue> terms;
+      if constexpr (kEpilogue) {
+        static_assert(LAYOUT == kDense && kTr && MAJ == 0, "epilogue of the dense NT layout");
+        if constexpr (EpilogueTerms<T>::kEarly) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
+      }
 
       lds_barrier();  // previous unit's readers are done with every LDS buffer
 
@@ -1136,17 +1173,22 @@ __global__ __launch_bounds__(T::kThreads) void gemm_kernel(GemmParams p, Schedul
       static_assert(kER * kRowBytes <= T::STAGES * T::kStageBytes, "epilogue tile does not fit");
       static_assert(kER == T::BM || kER == T::TM, "epilogue pass must be whole wave rows");
       const bool odd = fr & 1;
-      if constexpr (std::is_same_v<EPI, GemmEpilogue>) {
-        static_assert(LAYOUT == kDense && kTr && MAJ == 0, "epilogue of the dense NT layout");
-        apply_epilogue<T>(epi, acc, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
-      }
       // Round and pair up first: the packed words take half the registers
       // of the fp32 accumulators, which are dead from here on.
       uint32_t packed[T::FM][T::FN][2];
+      if constexpr (kEpilogue) {
+        if constexpr (!EpilogueTerms<T>::kEarly) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
+        apply_epilogue<T>(epi, terms, acc, packed, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
+      }
 #pragma unroll
       for (int i = 0; i < T::FM; ++i)
 #pragma unroll
         for (int j = 0; j < T::FN; ++j) {
+          if constexpr (kEpilogue) {
+            if constexpr (EpilogueTerms<T>::kWhole)
+              packed[i][j][0] = bf16_pair(acc[i][j][0], acc[i][j][1]), packed[i][j][1] = bf16_pair(acc[i][j][2], acc[i][j][3]);
+            continue;
+          }
           const uint32_t b0 = f32_to_bf16_rne(acc[i][j][0]), b1 = f32_to_bf16_rne(acc[i][j][1]);
           const uint32_t b2 = f32_to_bf16_rne(acc[i][j][2]), b3 = f32_to_bf16_rne(acc[i][j][3]);
           if constexpr (kTr) {  // columns 4kg, 4kg+1 | 4kg+2, 4kg+3 of row fr
