@@ -42,11 +42,14 @@ __device__ __forceinline__ float act_slope(float z) {
   } else if constexpr (ACT == DG_ACT_SILU) {
     return silu_slope(z, 1.0f, z, sigmoid(z));
   } else if constexpr (ACT == DG_ACT_GELU_TANH) {
-    // Past +-12 the slope is 1 or below 2^-126; t stays within the exponential's
-    // range up to there and z^2 finite.
-    const float v = __builtin_amdgcn_fmed3f(z, -12.0f, 12.0f), v2 = v * v;
-    const Sigmoid s = sigmoid(v * fmaf(kGelu3, v2, kGelu1));
-    return s.sig * fmaf(v * s.n, fmaf(3.0f * kGelu3, v2, kGelu1), 1.0f);
+    // Past +-9.5 the slope is 1 or below 2^-100; up to there t lies in +-77, where the
+    // exponential needs no limits of its own, and z^2 is finite.
+    const float v = __builtin_amdgcn_fmed3f(z, -9.5f, 9.5f), v2 = v * v;
+    const float t = v * fmaf(kGelu3, v2, kGelu1);
+    const float k = __builtin_rintf(t * kLog2e);
+    const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(fmaf(t, kLog2e, -k)), (int)k);
+    const float n = reciprocal(1.0f + e);  // 1 - sigmoid
+    return e * n * fmaf(v * n, fmaf(3.0f * kGelu3, v2, kGelu1), 1.0f);
   } else {
     return 1.0f;
   }
