@@ -40,20 +40,25 @@ __device__ __forceinline__ float inverse_root(float a) {
   return fmaf(y * 0.5f, fmaf(-a * y, y, 1.0f), y);
 }
 
-// Sums over a team of N values each.  Two calls one after another use different
+// Sums over a team of N values each: a row of 16 lanes, two of them, a wave, or a
+// workgroup.  Two calls one after another use different
 // words of shared memory (`turn`), so that one barrier a call is enough: the words
 // of a call are written again behind the barrier of the next one, which every wave
 // passes after it has read them.
 template <int TEAM>
 struct TeamSums {
-  static constexpr int kWaves = TEAM / 64;
+  static constexpr int kWaves = TEAM > 64 ? TEAM / 64 : 1;
   float words[2][kWaves][4];
 };
 
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sums(float (&v)[N], TeamSums<TEAM>& lds, int& turn) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+  for (int n = 0; n < N; ++n) {
+    if constexpr (TEAM >= 64) v[n] = wave_sum(v[n]);
+    else v[n] = row_sum(v[n]);
+    if constexpr (TEAM == 32) v[n] += __shfl_xor(v[n], 16, 64);
+  }
   if constexpr (TEAM > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -166,6 +171,13 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], const float (&rest
   }
 }
 
+// The team's number in its workgroup, in a scalar register where a wave has one.
+template <int TEAM>
+__device__ __forceinline__ int team_of_thread() {
+  const int team = threadIdx.x / TEAM;
+  return TEAM < 64 ? team : __builtin_amdgcn_readfirstlane(team);
+}
+
 // Threads of a workgroup: teams smaller than 256 threads share one.
 template <int TEAM>
 constexpr int kNormThreads = TEAM < 256 ? 256 : TEAM;
@@ -178,13 +190,13 @@ constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 template <bool POW2, bool STREAMING, int TEAM, int V>
 __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) {
   constexpr int kTeams = kNormThreads<TEAM> / TEAM;
-  static_assert(kTeams == 1 || TEAM == 64, "teams that share a workgroup are waves");
+  static_assert(kTeams == 1 || TEAM <= 64, "teams that share a workgroup need no barrier");
   __shared__ TeamSums<TEAM> lds;
   int turn = 0;
   const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
   const float inv_cols = 1.0f / (float)p.cols;
   const int64_t step = (int64_t)gridDim.x * kTeams;
-  for (int64_t t = (int64_t)blockIdx.x * kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM); t < p.tokens; t += step) {
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + team_of_thread<TEAM>(); t < p.tokens; t += step) {
     uint4 y[V], h[V];
     load_chunks(p.y + t * p.ld_y, c, y);
     if (p.h) load_chunks(p.h + t * p.ld_h, c, h);
@@ -354,7 +366,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
   float dw[V][8] = {}, db[EXTRA ? V : 1][8] = {}, dpw[POST ? V : 1][8] = {}, dg[EXTRA ? V : 1][8] = {};
   NormBwdRaw<V> raw = {}, next = {};
   const int64_t step = (int64_t)gridDim.x * kTeams;
-  int64_t t = (int64_t)blockIdx.x * kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+  int64_t t = (int64_t)blockIdx.x * kTeams + team_of_thread<TEAM>();
   if (kAhead && t < p.tokens) load_raw(p, t, read_y, c, next);
   for (; t < p.tokens; t += step) {
     if constexpr (kAhead) {
@@ -565,7 +577,9 @@ void go_norm(const NormParams& p, hipStream_t stream) {
 template <bool POW2, bool STREAMING>
 void pick_norm(const NormParams& p, hipStream_t stream) {
   const int chunks = p.cols / 8;
-  if (chunks <= 64) go_norm<POW2, STREAMING, 64, 1>(p, stream);
+  if (chunks <= 16) go_norm<POW2, STREAMING, 16, 1>(p, stream);
+  else if (chunks <= 32) go_norm<POW2, STREAMING, 32, 1>(p, stream);
+  else if (chunks <= 64) go_norm<POW2, STREAMING, 64, 1>(p, stream);
   else if (chunks <= 128) go_norm<POW2, STREAMING, 64, 2>(p, stream);
   else if (chunks <= 256) go_norm<POW2, STREAMING, 256, 1>(p, stream);
   else if (chunks <= 512) go_norm<POW2, STREAMING, 256, 2>(p, stream);
@@ -594,7 +608,7 @@ void pick_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
 
 // Rows that a workgroup of the gradient has at a time, and how many workgroups it
 // takes to fill the card.
-int teams_of(int cols) { return cols <= 1024 ? 8 : 1; }
+int teams_of(int cols) { return cols <= 128 ? 32 : cols <= 256 ? 16 : cols <= 1024 ? 8 : 1; }
 int most_parts(int cols) { return cols <= 1024 ? 256 : cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256; }
 
 }  // namespace
@@ -614,7 +628,9 @@ int norm_bwd_parts(int tokens, int cols) {
 hipError_t launch_block_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
   const int chunks = p.cols / 8;
   if (p.tokens > 0) {
-    if (chunks <= 64) pick_norm_bwd<64, 1>(p, stream);
+    if (chunks <= 16) pick_norm_bwd<16, 1>(p, stream);
+    else if (chunks <= 32) pick_norm_bwd<32, 1>(p, stream);
+    else if (chunks <= 64) pick_norm_bwd<64, 1>(p, stream);
     else if (chunks <= 128) pick_norm_bwd<64, 2>(p, stream);
     else if (chunks <= 256) pick_norm_bwd<256, 1>(p, stream);
     else if (chunks <= 512) pick_norm_bwd<512, 1>(p, stream);

@@ -78,7 +78,7 @@ BAD = [
     ("dg_block_norm_bwd", dict(gate=0, gate_kind=0), INVALID), ("dg_block_norm_bwd", dict(dy=0), INVALID),
     ("dg_block_norm_bwd", dict(r=0), INVALID), ("dg_block_norm_bwd", dict(y=0), INVALID), ("dg_block_norm_bwd", dict(ld_dr=504), INVALID),
     ("dg_block_norm_bwd", dict(ld_dy=516), MISALIGNED), ("dg_block_norm_bwd", dict(dgate=FAKE + 4), MISALIGNED),
-    ("dg_block_norm_bwd", dict(dweight=FAKE + 8), MISALIGNED), ("dg_block_norm_bwd", dict(workspace_bytes=4 * 16 * 512 * 4 - 1), WORKSPACE),
+    ("dg_block_norm_bwd", dict(dweight=FAKE + 8), MISALIGNED), ("dg_block_norm_bwd", dict(workspace_bytes=4 * 8 * 512 * 4 - 1), WORKSPACE),
     ("dg_block_norm_bwd", dict(workspace=0), WORKSPACE), ("dg_block_norm_bwd", dict(workspace=FAKE + 8), MISALIGNED),
     ("dg_moe_balance", dict(tokens=-1), INVALID), ("dg_moe_balance", dict(experts=0), INVALID),
     ("dg_moe_balance", dict(experts=1032, ld_logits=1032), SHAPE), ("dg_moe_balance", dict(topk=0), INVALID),
@@ -135,8 +135,8 @@ def test_valid_arguments_reach_the_launch():
 
 def test_workspace_sizes():
     assert dg.dg_get_block_norm_bwd_workspace_size(0, 512) == 0
-    # four sums for each workgroup, which has four narrow rows at a time or one wide one
-    assert dg.dg_get_block_norm_bwd_workspace_size(64, 512) == 4 * 16 * 512 * 4
+    # four sums for each workgroup, which has several narrow rows at a time or one wide one
+    assert dg.dg_get_block_norm_bwd_workspace_size(64, 512) == 4 * 8 * 512 * 4
     assert dg.dg_get_block_norm_bwd_workspace_size(64, 2048) == 4 * 64 * 2048 * 4
     assert dg.dg_get_block_norm_bwd_workspace_size(10, 20000) == 0
     assert dg.dg_get_moe_balance_workspace_size(-1, 8) == 0 and dg.dg_get_moe_balance_workspace_size(8, 2000) == 0

@@ -39,7 +39,7 @@ def parameters(tokens, cols, seed, gate, bias, post):
     return out
 
 
-SIZES = [(1, 8, 0), (3, 40, 8), (5, 512, 0), (9, 1000, 16), (130, 1024, 0), (6, 1536, 0), (33, 2048, 8), (4, 3584, 0),
+SIZES = [(1, 8, 0), (3, 40, 8), (100, 128, 0), (37, 136, 8), (45, 256, 0), (5, 512, 0), (9, 1000, 16), (130, 1024, 0), (6, 1536, 0), (33, 2048, 8), (4, 3584, 0),
          (7, 4104, 8), (5, 6144, 0), (300, 7168, 0), (3, 8192, 0), (2, 8200, 0), (3, 16384, 8)]
 
 
@@ -125,7 +125,7 @@ def test_small_rows_reach_eps():
     assert np.abs(want[1]).max() < 1e-8
 
 
-BWD = [(0, 64, 0), (1, 8, 0), (3, 40, 8), (5, 512, 0), (9, 1000, 16), (1100, 136, 0), (130, 1024, 0), (257, 2048, 8),
+BWD = [(0, 64, 0), (1, 8, 0), (3, 40, 8), (1000, 128, 8), (333, 256, 0), (5, 512, 0), (9, 1000, 16), (1100, 136, 0), (130, 1024, 0), (257, 2048, 8),
        (4, 3584, 0), (7, 4104, 8), (300, 7168, 0), (2, 8200, 0), (3, 16384, 8)]
 
 
