@@ -56,10 +56,12 @@ def _quantised_weight(w):
 class MoELayer:
     """Experts w1 [E][2 inter][hidden] (gate rows, then up rows) and
     w2 [E][hidden][inter] in bf16.  All buffers are made here, for `tokens`
-    tokens and `capacity` expert rows (default: room for every choice)."""
+    tokens and `capacity` expert rows (default: room for every choice).  With
+    `balance` (the coefficient of the load-balance loss) the forward pass also
+    gives `counts`, `used` and `loss`, and the logits' gradient holds the loss'."""
 
     def __init__(self, w1, w2, tokens, topk, score="sigmoid", bias=None, expert_groups=1, topk_groups=1, scale=1.0,
-                 capacity=None):
+                 capacity=None, balance=0.0):
         self.experts, self.inter2, self.hidden = w1.shape
         self.inter, self.topk, self.tokens = self.inter2 // 2, topk, tokens
         self.w1, self.w2 = _quantised_weight(w1), _quantised_weight(w2)
@@ -90,6 +92,10 @@ class MoELayer:
         need = max(dg.dg_get_moe_plan_workspace_size(tokens, topk, self.experts),
                    dg.dg_get_moe_combine_bwd_workspace_size(m, h),
                    *(dg.dg_get_workspace_size(m, n, k, self.experts) for n, k in ((2 * i, h), (h, i), (i, h), (h, 2 * i))))
+        self.balance = dict(score=score, coef=balance) if balance else None
+        if balance:
+            self.counts, self.used, self.loss = _i32(1, self.experts), _i32(1), _f32(1)
+            need = max(need, dg.dg_get_moe_balance_workspace_size(tokens, self.experts))
         # The GEMMs want their workspace zero before its first use and leave it so; the others' is their own.
         self.gemm_ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
         self.ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
@@ -98,6 +104,8 @@ class MoELayer:
         """x [tokens][hidden] bf16, logits [tokens][experts] float32 -> y [tokens][hidden] bf16."""
         self.logits = logits
         dg.dg_moe_route(logits, self.ids, self.weights, **self.choice, **self.routing)
+        if self.balance:
+            dg.dg_moe_balance(logits, self.ids, self.counts, self.used, self.loss, workspace=self.ws, **self.balance)
         dg.dg_moe_plan_contiguous(self.ids, self.row_of, self.src, self.m_indices, self.k_offsets, workspace=self.ws)
         dg.dg_moe_dispatch(x, self.src, self.xq, self.xsf, topk=self.topk)
         dg.dg_grouped_contiguous_qout(self.xq, self.xsf, *self.w1, self.h, self.hq, self.hsf, self.m_indices,
@@ -119,6 +127,8 @@ class MoELayer:
         dg.dg_requant_t(self.xq, self.xsf, self.m_indices, self.xqt, self.xsft)
         dg.dg_k_grouped_nt(self.dhqt, self.dhsft, self.xqt, self.xsft, self.dw1, self.k_offsets)
         dg.dg_moe_route_bwd(self.logits, self.ids, self.dweights, self.dlogits, **self.routing)
+        if self.balance:
+            dg.dg_moe_balance_bwd(self.logits, self.counts, self.used, self.dlogits, self.topk, add=self.dlogits, **self.balance)
         return self.dx, self.dw1, self.dw2, self.dlogits
 
 
