@@ -66,7 +66,7 @@ enum { DG_GATE_NONE = 0, DG_GATE_COLUMN = 1, DG_GATE_TOKEN = 2 };
  * Rules: cols % 8 == 0 (% 128 == 0 with codes), at most 16384; lds >= cols,
  * multiples of 8; ld_sf >= tokens, a multiple of 4; eps a positive normal number;
  * data pointers and those of [cols] parameters 16-byte aligned, a token gate's
- * 4-byte.  Squares are float32: a normalised row stays below 2^60 in magnitude.
+ * 4-byte.  Squares are float32: a normalised row stays below 2^56 in magnitude.
  */
 int dg_block_norm(const uint16_t* y, const uint16_t* h, const float* gate, const float* post_weight,
                   const float* weight, const float* bias, uint16_t* r, uint16_t* x, uint8_t* q,

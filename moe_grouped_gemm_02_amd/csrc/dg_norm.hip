@@ -142,8 +142,8 @@ __device__ __forceinline__ float norm_scale(float (&v)[V][8], const Chunks<TEAM,
 
 // Codes of 8 values x + rest (rest: what the rounding of x left), a tile of 128 by 16
 // lanes.  The quotient takes in both residuals, so that a code differs from that of the
-// exact value only where that lies within a rounding of a boundary (4096 x 7168, of 29M
-// codes: GAIN).
+// exact value only where that lies within a rounding of a boundary (of 294M codes of
+// normal rows 273 differ, and 318 with the quotient of the rounded value alone).
 template <bool POW2>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], const float (&rest)[8], float& s, uint32_t& e) {
   float m = 0.0f;
@@ -184,6 +184,12 @@ constexpr int kNormThreads = TEAM < 256 ? 256 : TEAM;
 template <int TEAM>
 constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 
+// Bound by the memory: everything is read once and written once (16384 x 7168 with both
+// norms, gate, r and codes: 207 us, 5.1 TB/s, where a copy of 256 MiB reaches 5.2; one
+// row: 3.6 us, the launch).  The teams are the smallest that hold a row in 16 values a
+// thread, since a row's sums wait for its last load and other rows have to fill that
+// time: 512 threads for 7168 columns 207 us, 256 threads of 32 values 216, 1024 of 8
+// 262; 375000 rows of 128 columns 62 us by 16 lanes, 160 by a wave.
 // STREAMING: results larger than the L2s, which nothing reads back through them
 // (store_streaming; 4096 x 7168 with r, bf16 rows and codes: 49.0 us, and 54.5 with
 // plain stores).
@@ -298,13 +304,14 @@ __device__ __forceinline__ void load_raw(const NormBwdParams& p, int64_t t, bool
 
 // The parameters' columns (ones without a parameter), where reading them again for
 // each row waits for nothing but itself: loads from memory come back in order, so a
-// row's parameters would wait for the next row, which is on its way (16384 x 7168:
-// GAIN).  In registers, or in shared memory, first and second halves of the chunks
-// apart, so that lanes side by side read 16 bytes side by side; rows of more than 8192
-// values, which are not read ahead, take them from memory.
+// row's parameters would wait for the next row, which is on its way (16384 x 7168: 264
+// us, and 349 with parameters from memory).  In registers, or in shared memory, first
+// and second halves of the chunks apart, so that lanes side by side read 16 bytes side
+// by side; rows of more than 12288 values, which are not read ahead, take them from
+// memory.
 enum ColumnsIn { kRegisters, kShared, kMemory };
 template <int TEAM, int V>
-constexpr ColumnsIn kColumnsIn = TEAM * V > 1024 ? kMemory : V == 1 ? kRegisters : kShared;
+constexpr ColumnsIn kColumnsIn = TEAM * V > 1536 ? kMemory : V == 1 ? kRegisters : kShared;
 template <int TEAM, int V>
 struct ColumnsLds {
   float4 half[2][kColumnsIn<TEAM, V> == kShared ? V * TEAM : 1];
@@ -345,9 +352,51 @@ struct Columns {
   }
 };
 
+// The sums of a column gradient over a team's rows: in registers, or, where two norms
+// of rows of more than 12288 values leave none for them, each thread's in its own words
+// of shared memory (16384 columns, both norms and a column gate: 3.6 TB/s, and 1.7 with
+// sums that spill).
+template <int TEAM, int V, bool POST>
+constexpr bool kSumsInLds = POST && TEAM * V > 1536;
+template <int TEAM, int V, bool LDS>
+struct ColumnAcc {
+  float kept[LDS ? 1 : V][8] = {};
+  float4* half;  // [2][V * TEAM], as ColumnsLds
+  __device__ __forceinline__ ColumnAcc(float4* lds, const Chunks<TEAM, V>& c) : half(lds) {
+    if constexpr (LDS) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) half[c.at(i)] = half[V * TEAM + c.at(i)] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
+  __device__ __forceinline__ void add(const Chunks<TEAM, V>& c, int i, const float (&a)[8], const float (&b)[8]) {
+    if constexpr (LDS) {
+      float v[8];
+      get(c, i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = fmaf(a[e], b[e], v[e]);
+      half[c.at(i)] = make_float4(v[0], v[1], v[2], v[3]);
+      half[V * TEAM + c.at(i)] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kept[i][e] = fmaf(a[e], b[e], kept[i][e]);
+    }
+  }
+  __device__ __forceinline__ void get(const Chunks<TEAM, V>& c, int i, float (&v)[8]) const {
+    if constexpr (LDS) {
+      const float4 a = half[c.at(i)], b = half[V * TEAM + c.at(i)];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = kept[i][e];
+    }
+  }
+};
+
 // Gradient.  Each team walks down the rows and keeps the sums over its rows of the
-// column gradients in registers; they leave once, as a row of partial sums of the
-// workgroup.  The next row is read while this one is worked on.  POST, LAYER: as in
+// column gradients; they leave once, as a row of partial sums of the workgroup, so that
+// the sums need no atomics and their order is fixed.  Bound by the memory: 16384 x 7168
+// with both norms 264 us, 5.4 TB/s; 4.9 to 5.5 TB/s up to 8192 columns, and above, where
+// registers run short, 3.8 to 5.3 up to 12288 and 3.1 to 4.3 up to 16384.  The next row is read while this one is worked on.  POST, LAYER: as in
 // the call; EXTRA: whether the gradients of a bias or of a column gate are wanted
 // (registers for two more sums).
 template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
@@ -358,12 +407,16 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
   const Chunks<TEAM, V> c = {(int)threadIdx.x % TEAM, p.cols / 8};
   const float inv_cols = 1.0f / (float)p.cols;
   const bool read_y = POST || p.dgate;
-  constexpr bool kAhead = TEAM * V <= 1024;  // 128 registers of 1024 threads do not hold a second row
+  // A second row where the registers hold it.
+  constexpr bool kAhead = TEAM * V <= 1024 || (TEAM * V <= 1536 && !(POST && EXTRA));
   __shared__ ColumnsLds<TEAM, V> columns[3];
   const Columns<TEAM, V> weight(p.weight, columns[0], c), post_weight(POST ? p.post_weight : nullptr, columns[1], c),
       gate(p.gate_kind == DG_GATE_COLUMN ? p.gate : nullptr, columns[2], c);
   __syncthreads();
-  float dw[V][8] = {}, db[EXTRA ? V : 1][8] = {}, dpw[POST ? V : 1][8] = {}, dg[EXTRA ? V : 1][8] = {};
+  constexpr bool kLds = kSumsInLds<TEAM, V, POST>;
+  __shared__ float4 sums[kLds ? 2 : 1][kLds ? 2 * V * TEAM : 1];
+  ColumnAcc<TEAM, V, kLds> dw(sums[0], c), dpw(sums[kLds ? 1 : 0], c);
+  ColumnAcc<TEAM, V, false> db(nullptr, c), dg(nullptr, c);
   NormBwdRaw<V> raw = {}, next = {};
   const int64_t step = (int64_t)gridDim.x * kTeams;
   int64_t t = (int64_t)blockIdx.x * kTeams + team_of_thread<TEAM>();
@@ -440,17 +493,17 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
       }
       if (!c.in(i)) continue;
       if (p.dx) {
-        float a[8], b[8], w[8];
-        widen8(raw.r[i], a);
+        float n[8], b[8], w[8];
+        widen8(raw.r[i], n);
         widen8(raw.dx[i], b);
         weight.get(c, i, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float n = (a[e] - mean_r) * kr;
-          dw[i][e] = fmaf(b[e], n, dw[i][e]);
-          if constexpr (EXTRA) db[i][e] += b[e];
-          tot[i][e] = fmaf(kr, fmaf(-n, gn, fmaf(b[e], w[e], -mean_g)), tot[i][e]);
+          n[e] = (n[e] - mean_r) * kr;
+          if constexpr (EXTRA) db.kept[i][e] += b[e];
+          tot[i][e] = fmaf(kr, fmaf(-n[e], gn, fmaf(b[e], w[e], -mean_g)), tot[i][e]);
         }
+        dw.add(c, i, b, n);
       }
       if (p.dh) {
         float out[8];
@@ -471,7 +524,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float tu = tot[i][e] * (POST ? yv[e] * pw[e] : yv[e]);
-            if constexpr (EXTRA) dg[i][e] += tu;
+            if constexpr (EXTRA) dg.kept[i][e] += tu;
             after[2] += tu;
           }
         }
@@ -479,9 +532,9 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
 #pragma unroll
       for (int e = 0; e < 8; ++e) tot[i][e] *= g[e] * token_gate;
       if constexpr (POST) {
+        dpw.add(c, i, tot[i], yv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dpw[i][e] = fmaf(tot[i][e], yv[e], dpw[i][e]);
           tot[i][e] *= pw[e];
           after[0] += tot[i][e];
           after[1] = fmaf(tot[i][e], yv[e], after[1]);
@@ -505,16 +558,19 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
   }
   // The workgroup's row of partial sums; waves with rows of their own come together
   // in shared memory, in order.
-  auto leave = [&](float (&sum)[V][8], float* to) {
+  auto leave = [&](auto get, float* to) {
     if (!to) return;
     to += (int64_t)blockIdx.x * p.cols;
     if constexpr (kTeams > 1) {
       __shared__ float rows[kTeams][V * TEAM * 8];
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i) {
+        float sum[8];
+        get(i, sum);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rows[threadIdx.x / TEAM][c.at(i) * 8 + e] = sum[i][e];
+        for (int e = 0; e < 8; ++e) rows[threadIdx.x / TEAM][c.at(i) * 8 + e] = sum[e];
+      }
       __syncthreads();
       for (int col = threadIdx.x; col < p.cols; col += kBwdThreads<TEAM>) {
         float all = rows[0][col];
@@ -526,21 +582,25 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (!c.in(i)) continue;
+        float sum[8];
+        get(i, sum);
         float4* at = reinterpret_cast<float4*>(to + c.at(i) * 8);
-        at[0] = make_float4(sum[i][0], sum[i][1], sum[i][2], sum[i][3]);
-        at[1] = make_float4(sum[i][4], sum[i][5], sum[i][6], sum[i][7]);
+        at[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        at[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
       }
     }
   };
   const int64_t matrix = (int64_t)gridDim.x * p.cols;
-  leave(dw, p.dweight ? p.parts : nullptr);
-  if constexpr (EXTRA) leave(db, p.dbias ? p.parts + matrix : nullptr);
-  if constexpr (POST) leave(dpw, p.dpost_weight ? p.parts + 2 * matrix : nullptr);
-  if constexpr (EXTRA) leave(dg, p.dgate && p.gate_kind == DG_GATE_COLUMN ? p.parts + 3 * matrix : nullptr);
+  auto of = [&](const auto& sum) { return [&](int i, float (&v)[8]) { sum.get(c, i, v); }; };
+  leave(of(dw), p.dweight ? p.parts : nullptr);
+  if constexpr (EXTRA) leave(of(db), p.dbias ? p.parts + matrix : nullptr);
+  if constexpr (POST) leave(of(dpw), p.dpost_weight ? p.parts + 2 * matrix : nullptr);
+  if constexpr (EXTRA) leave(of(dg), p.dgate && p.gate_kind == DG_GATE_COLUMN ? p.parts + 3 * matrix : nullptr);
 }
 
 // Workgroup (x, y): 64 columns of matrix y, 16 threads wide (4 columns each) and 16
-// rows tall; the rows' sums come together in shared memory.
+// rows tall; the rows' sums come together in shared memory.  Bound by latency: 256 rows
+// of 7168 columns 4 us, of which 3.7 are the launch's.
 __global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums s) {
   __shared__ float4 rows[16][16];
   const float* from = s.from[blockIdx.y];
@@ -635,7 +695,8 @@ hipError_t launch_block_norm_bwd(const NormBwdParams& p, hipStream_t stream) {
     else if (chunks <= 256) pick_norm_bwd<256, 1>(p, stream);
     else if (chunks <= 512) pick_norm_bwd<512, 1>(p, stream);
     else if (chunks <= 1024) pick_norm_bwd<512, 2>(p, stream);
-    else pick_norm_bwd<1024, 2>(p, stream);
+    else if (chunks <= 1536) pick_norm_bwd<512, 3>(p, stream);
+    else pick_norm_bwd<512, 4>(p, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -4,6 +4,7 @@ its rules are refused on the host, with a message, before anything is enqueued."
 
 import ctypes
 import os
+import random
 import re
 import subprocess
 
@@ -131,6 +132,26 @@ def test_valid_arguments_reach_the_launch():
     for name in DECLS:
         if not name.startswith("dg_get_"):
             assert call(name) == -5, name
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the launches would run on fake addresses")
+@pytest.mark.parametrize("cus", [8, 64, 104, 256])
+def test_every_shape_has_a_tile_with_an_epilogue(cus):
+    """Whatever the selection takes for a dense product exists with an epilogue: every valid call gets as far as the launch."""
+    rng = random.Random(cus)
+    dg.dg_set_num_cus(cus)
+    try:
+        for _ in range(3000):
+            m, n = (int(2 ** rng.uniform(0, 15)) for _ in range(2))
+            k, ue, codes = 128 * int(2 ** rng.uniform(0, 7.5)), rng.random() < 0.5, rng.random() < 0.3
+            n = -(-n // 128) * 128 if codes else n
+            ld = -(-n // 8) * 8
+            quantised = {} if codes else dict(dq=0, dsf=0)
+            status = call("dg_fp8_gemm_nt_ue8m0_epilogue" if ue else "dg_fp8_gemm_nt_epilogue", m=m, n=n, k=k, lda=k, ldb=k, ldd=ld,
+                          ld_sfa=-(-m // 4) * 4, ld_res=ld, ld_pre=ld, ld_dsf=-(-m // 4) * 4, **quantised)
+            assert status == -5 and "launch" in dg.dg_get_last_error_string(), (m, n, k, ue, codes, dg.dg_get_last_error_string())
+    finally:
+        dg.dg_set_num_cus(0)
 
 
 def test_workspace_sizes():

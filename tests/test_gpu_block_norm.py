@@ -126,7 +126,7 @@ def test_small_rows_reach_eps():
 
 
 BWD = [(0, 64, 0), (1, 8, 0), (3, 40, 8), (1000, 128, 8), (333, 256, 0), (5, 512, 0), (9, 1000, 16), (1100, 136, 0), (130, 1024, 0), (257, 2048, 8),
-       (4, 3584, 0), (7, 4104, 8), (300, 7168, 0), (2, 8200, 0), (3, 16384, 8)]
+       (4, 3584, 0), (7, 4104, 8), (300, 7168, 0), (2, 8200, 0), (3, 16384, 8), (770, 8200, 0), (300, 12288, 8), (520, 16384, 0)]
 
 
 @pytest.mark.parametrize("tokens,cols,pad", BWD, ids=str)
