@@ -7,9 +7,8 @@
 // chunk, a row of sums over their common tokens: chunk b and sequence s share row
 // b + s (both only grow along the tokens, so no two pairs have the same), and a
 // second launch adds the rows of each sequence in their order.  32768 tokens of 256
-// fp32 experts: 13.4 + 6.5 us, and 20.5 for the gradient, which reads 34 MB (from the
-// caches that the forward pass left them in) and writes as much.  Bound by latency and
-// exponentials: the logits are read at 2.5 TB/s.
+// fp32 experts: 8.5 + 6.4 us (13.4 + 6.5 with every score formed as the gradient's), and
+// 20 for the gradient, which reads 34 MB and writes as much.
 
 #include "dg_block_internal.h"
 #include "dg_math.h"
@@ -108,10 +107,66 @@ __device__ __forceinline__ bool shares(const float (&x)[V], float (&p)[V], float
   return __ballot(open) != 0;
 }
 
+// Rows as they nearly always are: no NaN, the largest logit finite and, for sigmoid
+// scores, one of them not negative, so that no score has to be taken relative to
+// another one.  top: the largest logit (softmax).
+template <int V>
+__device__ __forceinline__ bool ordinary(const float (&x)[V], bool sigmoid_scores, float& top) {
+  float most = x[0];
+  bool nan = x[0] != x[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) most = fmaxf(most, x[i]);
+#pragma unroll
+  for (int i = 1; i < V; i += 2) nan |= __builtin_isunordered(x[i], x[i + 1 < V ? i + 1 : i]);
+  if (__ballot(nan)) return false;
+  if (sigmoid_scores) return __ballot(most >= 0.0f) != 0;
+  const uint32_t all = wave_max(order_of(most));
+  top = of_order(all);
+  return all != 0 && top < INFINITY;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// What shares of an ordinary row are proportional to, for sums over tokens: the
+// hardware's 2^x of the product as it was rounded, within |x| 2^-24 of the value, and
+// 0 where that is below the normal range.
+template <int V>
+__device__ __forceinline__ float weights(const float (&x)[V], float top, bool sigmoid_scores, float (&p)[V]) {
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    p[i] = sigmoid_scores ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x[i]))
+                          : __builtin_amdgcn_exp2f(kLog2e * (x[i] - top));
+    total += p[i];
+  }
+  return wave_sum(total);
+}
+
+// The same within 3 ulp, results below the normal range included, and that times
+// the slope's factor: s (1 - s) is the same on both sides of 0.
+template <int V>
+__device__ __forceinline__ void slopes(const float (&x)[V], float top, bool sigmoid_scores, float (&p)[V], float (&g)[V]) {
+  auto e_to = [](float v) {  // exp_to_80 of v <= 0 that is a number
+    v = fmaxf(v, -150.0f);
+    const float k = __builtin_rintf(v * kLog2e);
+    return __builtin_ldexpf(__builtin_amdgcn_exp2f(fmaf(v, kLog2e, -k)), (int)k);
+  };
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (sigmoid_scores) {
+      const float e = e_to(-fabsf(x[i])), large = __builtin_amdgcn_rcpf(1.0f + e), small = e * large;
+      p[i] = x[i] < 0.0f ? small : large;
+      g[i] = small * large;
+    } else {
+      p[i] = g[i] = e_to(x[i] - top);
+    }
+  }
+}
+
 // Workgroup: a chunk of tokens, its waves one token after another, the next one read
 // ahead (four ahead measure the same, and take registers).  At most 256 chunks: few rows
-// for the second launch to add (32768 x 256: 13.4 us here and 6.5 there, against 13.2
-// and 12.6 with 1024 chunks of 4 waves), one workgroup a CU, which reads its 131 KB at
+// for the second launch to add (32768 x 256: 6.5 us there, against 12.6 with 1024
+// chunks of 4 waves, which take as long here), one workgroup a CU, which reads its 131 KB at
 // what a CU reaches.
 constexpr int kSumWaves = 16, kMostChunks = 256;
 
@@ -136,17 +191,23 @@ __global__ __launch_bounds__(64 * kSumWaves) void balance_kernel(BalanceParams p
     if (from + wave < to) fetch(from + wave);
     __syncthreads();
     for (int t = from + wave; t < to; t += kSumWaves) {
-      float x[V], share[V], rest[V];
+      float x[V], share[V], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = next[i];
       const int id = next_id;
       if (t + kSumWaves < to) fetch(t + kSumWaves);
       arrange_row<VEC>(lane, sums[wave], x);
-      if (!shares<V>(x, share, rest, p.sigmoid != 0)) continue;
+      float inv = 1.0f;
+      if (ordinary<V>(x, p.sigmoid != 0, top)) {
+        inv = reciprocal(p.sigmoid ? weights<V>(x, top, true, share) : weights<V>(x, top, false, share));
+      } else {
+        float rest[V];
+        if (!shares<V>(x, share, rest, p.sigmoid != 0)) continue;
+      }
       ++here;
-      if (id >= 0 && id < p.experts) atomicAdd(&counts[id], 1);
+      if ((uint32_t)id < (uint32_t)p.experts) atomicAdd(&counts[id], 1);
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += share[i];
+      for (int i = 0; i < V; ++i) sum[i] = fmaf(share[i], inv, sum[i]);
     }
     wave_fence();
 #pragma unroll
@@ -237,7 +298,10 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
   }
 }
 
-constexpr int kWaves = 4, kBwdChunk = 16;  // waves and tokens of a workgroup
+// Waves and tokens of a workgroup of the gradient.  Bound by the vector units, 172
+// instructions a token of 256 experts (32 tokens 21.0 us, 16 tokens 20; the same with
+// all of a wave's rows read before its sequence is known, so it does not wait for them).
+constexpr int kWaves = 4, kBwdChunk = 16;
 
 template <bool VEC, typename T, int V>
 __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams p) {
@@ -260,18 +324,29 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams 
       f[i] = e < p.experts ? per * (float)p.counts[(int64_t)s * p.experts + e] : 0.0f;
     }
     for (int t = from + wave; t < to; t += kWaves) {
-      float x[V], add[V], share[V], rest[V];
+      float x[V], add[V], share[V], g[V], top = 0.0f;
       load_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, rows[wave], x);
       if (p.add) load_row<VEC>(static_cast<const T*>(p.add) + (int64_t)t * p.ld_add, p.experts, lane, rows[wave], add);
-      shares<V>(x, share, rest, p.sigmoid != 0);
-      float mean = 0.0f;
+      const bool usual = ordinary<V>(x, p.sigmoid != 0, top);
+      if (usual) {
+        p.sigmoid ? slopes<V>(x, top, true, share, g) : slopes<V>(x, top, false, share, g);
+      } else {
+        float rest[V];
+        shares<V>(x, share, rest, p.sigmoid != 0);
 #pragma unroll
-      for (int i = 0; i < V; ++i) mean = fmaf(f[i], share[i], mean);
-      mean = wave_sum(mean);
+        for (int i = 0; i < V; ++i) g[i] = share[i] * rest[i];
+      }
+      float total = 0.0f, mean = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) total += share[i], mean = fmaf(f[i], share[i], mean);
+      total = wave_sum(total);
+      const float inv = usual ? reciprocal(total) : 1.0f;
+      mean = wave_sum(mean) * inv;
+      const float scale = a * inv;
       float out[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        out[i] = a * (share[i] * rest[i] * (f[i] - mean));
+        out[i] = scale * (g[i] * (f[i] - mean));
         if (p.add) out[i] += add[i];
       }
       T* to_row = static_cast<T*>(p.dlogits) + (int64_t)t * p.ld_d;
