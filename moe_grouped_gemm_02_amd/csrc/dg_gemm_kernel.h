@@ -335,43 +335,121 @@ __device__ __forceinline__ const float* scale_ptr(const float* base, int64_t off
   return base + offset;
 }
 
-// What an epilogue adds to the wave's sums: the lane's row of fragment i is
-// row0 + 16 i, its columns of fragment j col0 + 16 j .. + 3.  Tiles of up to 8
-// fragments a wave read all of it before their K loop, which hides the wait (128 x 7168 x
-// 16384 with bias and residual: 43.9 -> 41.5 us), those of up to 20 at once behind it
-// (4096 x 2112 x 7168 with all terms: 90.5 us, 96.9 a row ahead).  The 256 x 256 tile's
-// 32 fragments leave registers for two rows of the residual, which is read a row ahead
-// (4096 x 4096 x 7168 with UE8M0 scales and all terms: 121 us, 126 at once).
+// Matrix rows next to the wave's sums.  A lane has columns 4 kg .. 4 kg + 3 of each
+// fragment, 8 bytes; of two fragments side by side it reads or writes 16 bytes of one of
+// them, and swaps half with the lane 16 further (rows 1 and 3 of 16 lanes against 0 and
+// 2): half the accesses (4096 x 7168 x 2048 with all terms: 122 -> 106 us).  Tiles of 4
+// fragments a wave leave it at 8 bytes: they are calls of few rows, which wait for one
+// access and not for their number (1 x 7168 x 2048: 9.1 us, 9.7 in pairs).
 template <class T>
-struct EpilogueTerms {
-  static constexpr bool kEarly = T::FM * T::FN <= 8, kWhole = T::FM * T::FN <= 20;
-  float bias[T::FN][4];
-  uint2 residual[kWhole ? T::FM : 2][T::FN];
-  // Four bf16 values of fragment row i, or as many as the matrix has.
-  __device__ __forceinline__ void load_row(const GemmEpilogue& e, int i, int row0, int col0, int m, int n) {
-    if (!kWhole && !e.residual) return;
-    const int row = row0 + 16 * i;
-    const uint16_t* from = e.residual + (int64_t)row * e.ld_res;
+struct FragmentRow {
+  static constexpr int kPairs = T::FM * T::FN <= 4 ? 0 : T::FN / 2;
+  static __device__ __forceinline__ void swap(uint32_t& a, uint32_t& b) {
+    const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = v[0], b = v[1];
+  }
+  static __device__ __forceinline__ int pair_col(int col0) {
+    const int kg = (threadIdx.x >> 4) & 3;
+    return col0 - 4 * kg + 16 * (kg & 1) + 8 * (kg >> 1);
+  }
+  // The lane's values as they were read, 0 past the last column; arranged() hands them
+  // out, apart from the load, which it would wait for.
+  static __device__ __forceinline__ void load(const uint16_t* from, bool in, int col0, int n, uint2 (&v)[T::FN]) {
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) {
+    for (int q = 0; q < kPairs; ++q) {
+      const int col = pair_col(col0) + 32 * q;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (in && col + 7 < n) w = *reinterpret_cast<const uint4*>(from + col);
+      else if (in && col < n) {
+        uint32_t e[7];
+#pragma unroll
+        for (int c = 0; c < 7; ++c) e[c] = col + c < n ? from[col + c] : 0u;
+        w = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6]);
+      }
+      v[2 * q] = make_uint2(w.x, w.y), v[2 * q + 1] = make_uint2(w.z, w.w);
+    }
+#pragma unroll
+    for (int j = 2 * kPairs; j < T::FN; ++j) {
       const int col = col0 + 16 * j;
-      uint2& to = residual[kWhole ? i : i & 1][j];
+      uint2& to = v[j];
       to = make_uint2(0, 0);
-      if (!e.residual || row >= m) continue;
-      if (col + 3 < n) {
-        to = *reinterpret_cast<const uint2*>(from + col);
-      } else {
-        uint32_t v[3] = {0, 0, 0};
+      if (in && col + 3 < n) to = *reinterpret_cast<const uint2*>(from + col);
+      else if (in && col < n) {
+        uint32_t e[3];
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
-          if (col + c < n) v[c] = from[col + c];
-        to = make_uint2(v[0] | (v[1] << 16), v[2]);
+        for (int c = 0; c < 3; ++c) e[c] = col + c < n ? from[col + c] : 0u;
+        to = make_uint2(e[0] | (e[1] << 16), e[2]);
       }
     }
   }
+  static __device__ __forceinline__ void arranged(uint2 (&v)[T::FN]) {
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+      swap(v[2 * q].x, v[2 * q + 1].x);
+      swap(v[2 * q].y, v[2 * q + 1].y);
+    }
+  }
+  static __device__ __forceinline__ void store(uint16_t* to, bool in, int col0, int n, uint2 (&v)[T::FN]) {
+    arranged(v);
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+      const int col = pair_col(col0) + 32 * q;
+      const uint4 w = make_uint4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+      if (in && col + 7 < n) *reinterpret_cast<uint4*>(to + col) = w;
+      else if (in && col < n) {
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c = 0; c < 7; ++c)
+          if (col + c < n) to[col + c] = (uint16_t)(e[c / 2] >> (16 * (c & 1)));
+      }
+    }
+#pragma unroll
+    for (int j = 2 * kPairs; j < T::FN; ++j) {
+      const int col = col0 + 16 * j;
+      const uint2 w = v[j];
+      if (in && col + 3 < n) *reinterpret_cast<uint2*>(to + col) = w;
+      else if (in && col < n) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (col + c < n) to[col + c] = (uint16_t)((c < 2 ? w.x : w.y) >> (16 * (c & 1)));
+      }
+    }
+  }
+};
+
+// What an epilogue adds to the wave's sums: the lane's row of fragment i is
+// row0 + 16 i, its columns of fragment j col0 + 16 j .. + 3.  Tiles of 4 fragments a wave
+// read all of it before their K loop, which hides the wait (128 x 4096 x 7168 with
+// bias, residual and activation: 16.3 us, 17.0 behind it), those of 8 too where the K axis is
+// not divided: joining the parts takes the registers (1000 x 2112 x 7168: 35.7 us behind the
+// join, 39.0 before the K loop).  Those of up to 20 read it at once behind the loop (4096 x
+// 2112 x 7168 with all terms: 88.6 us, 96.9 a row ahead).  The 256 x 256 tile's 32
+// fragments leave registers for two rows of the residual, which is read a row ahead
+// (4096 x 4096 x 7168 with UE8M0 scales and all terms: 121 us, 126 at once, 122 two rows
+// ahead; 115 with 16-byte accesses).
+template <class T>
+struct EpilogueTerms {
+  static constexpr int kFragments = T::FM * T::FN;
+  static constexpr bool kWhole = kFragments <= 20;
+  template <bool SK>
+  static constexpr bool kBeforeLoop = kFragments <= (SK ? 4 : 8);
+  static constexpr int kRows = kWhole ? T::FM : 2;  // rows of the residual that are held
+  float bias[T::FN][4];
+  uint2 residual[kRows][T::FN];
+  __device__ __forceinline__ void load_row(const GemmEpilogue& e, int i, int row0, int col0, int m, int n) {
+    if (!e.residual) {
+      if (kWhole) {
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) residual[i % kRows][j] = make_uint2(0, 0);
+      }
+      return;
+    }
+    const int row = row0 + 16 * i;
+    FragmentRow<T>::load(e.residual + (int64_t)row * e.ld_res, row < m, col0, n, residual[i % kRows]);
+  }
   __device__ __forceinline__ void load(const GemmEpilogue& e, int row0, int col0, int m, int n) {
 #pragma unroll
-    for (int i = 0; i < (kWhole ? T::FM : 1); ++i) load_row(e, i, row0, col0, m, n);
+    for (int i = 0; i < (kWhole ? T::FM : kRows - 1); ++i) load_row(e, i, row0, col0, m, n);
 #pragma unroll
     for (int j = 0; j < T::FN; ++j)
 #pragma unroll
@@ -389,27 +467,20 @@ __device__ __forceinline__ void apply_epilogue(const GemmEpilogue& e, EpilogueTe
                                                uint32_t (&packed)[T::FM][T::FN][2], int row0, int col0, int m, int n) {
   static_for<T::FM>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
-    if constexpr (!EpilogueTerms<T>::kWhole && i + 1 < T::FM) terms.load_row(e, i + 1, row0, col0, m, n);
-    const uint2(&res)[T::FN] = terms.residual[EpilogueTerms<T>::kWhole ? i : i & 1];
+    constexpr int kAhead = EpilogueTerms<T>::kRows - 1;
+    if constexpr (!EpilogueTerms<T>::kWhole && i + kAhead < T::FM) terms.load_row(e, i + kAhead, row0, col0, m, n);
+    uint2(&res)[T::FN] = terms.residual[i % EpilogueTerms<T>::kRows];
     float z[T::FN][4];
 #pragma unroll
     for (int j = 0; j < T::FN; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c) z[j][c] = acc[i][j][c] + terms.bias[j][c];
-    if (e.pre && row0 + 16 * i < m) {
-      uint16_t* to = e.pre + (int64_t)(row0 + 16 * i) * e.ld_pre;
+    if (e.pre) {
+      uint2 v[T::FN];
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j) {
-        const int col = col0 + 16 * j;
-        const uint32_t lo = bf16_pair(z[j][0], z[j][1]), hi = bf16_pair(z[j][2], z[j][3]);
-        if (col + 3 < n) {
-          *reinterpret_cast<uint2*>(to + col) = make_uint2(lo, hi);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            if (col + c < n) to[col + c] = (uint16_t)((c < 2 ? lo : hi) >> ((c & 1) * 16));
-        }
-      }
+      for (int j = 0; j < T::FN; ++j) v[j] = make_uint2(bf16_pair(z[j][0], z[j][1]), bf16_pair(z[j][2], z[j][3]));
+      const int row = row0 + 16 * i;
+      FragmentRow<T>::store(e.pre + (int64_t)row * e.ld_pre, row < m, col0, n, v);
     }
     with_act(e.act, [&](auto act) {
 #pragma unroll
@@ -419,6 +490,7 @@ __device__ __forceinline__ void apply_epilogue(const GemmEpilogue& e, EpilogueTe
     });
     // (A branch here costs the 256 x 160 tile 70 spilled registers: zeros are added.)
     if (EpilogueTerms<T>::kWhole || e.residual) {
+      FragmentRow<T>::arranged(res);
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) {
         z[j][0] += __uint_as_float(res[j].x << 16);
@@ -782,7 +854,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_kernel(GemmParams p, Schedul
       std::conditional_t<kEpilogue, EpilogueTerms<T>, NoEpilogue> terms;
       if constexpr (kEpilogue) {
         static_assert(LAYOUT == kDense && kTr && MAJ == 0, "epilogue of the dense NT layout");
-        if constexpr (EpilogueTerms<T>::kEarly) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
+        if constexpr (EpilogueTerms<T>::template kBeforeLoop<SK>) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
       }
 
       lds_barrier();  // previous unit's readers are done with every LDS buffer
@@ -1177,7 +1249,7 @@ __global__ __launch_bounds__(T::kThreads) void gemm_kernel(GemmParams p, Schedul
       // of the fp32 accumulators, which are dead from here on.
       uint32_t packed[T::FM][T::FN][2];
       if constexpr (kEpilogue) {
-        if constexpr (!EpilogueTerms<T>::kEarly) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
+        if constexpr (!EpilogueTerms<T>::template kBeforeLoop<SK>) terms.load(epi, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
         apply_epilogue<T>(epi, terms, acc, packed, m0 + wm * T::TM + fr, n0 + wn * T::TN + 4 * kg, p.m, p.n);
       }
 #pragma unroll
