@@ -338,7 +338,8 @@ __device__ __forceinline__ const float* scale_ptr(const float* base, int64_t off
 // Matrix rows next to the wave's sums.  A lane has columns 4 kg .. 4 kg + 3 of each
 // fragment, 8 bytes; of two fragments side by side it reads or writes 16 bytes of one of
 // them, and swaps half with the lane 16 further (rows 1 and 3 of 16 lanes against 0 and
-// 2): half the accesses (4096 x 7168 x 2048 with all terms: 122 -> 106 us).  Tiles of 4
+// 2): half the accesses (4096 x 7168 x 2048 with UE8M0 scales: 70.5 -> 65.4 us without a
+// term, 115 -> 97 with all of them).  Tiles of 4
 // fragments a wave leave it at 8 bytes: they are calls of few rows, which wait for one
 // access and not for their number (1 x 7168 x 2048: 9.1 us, 9.7 in pairs).
 template <class T>
@@ -421,9 +422,9 @@ struct FragmentRow {
 // row0 + 16 i, its columns of fragment j col0 + 16 j .. + 3.  Tiles of 4 fragments a wave
 // read all of it before their K loop, which hides the wait (128 x 4096 x 7168 with
 // bias, residual and activation: 16.3 us, 17.0 behind it), those of 8 too where the K axis is
-// not divided: joining the parts takes the registers (1000 x 2112 x 7168: 35.7 us behind the
-// join, 39.0 before the K loop).  Those of up to 20 read it at once behind the loop (4096 x
-// 2112 x 7168 with all terms: 88.6 us, 96.9 a row ahead).  The 256 x 256 tile's 32
+// not divided: joining the parts takes the registers (1000 x 2112 x 7168 with 8-byte
+// accesses: 36.3 us behind the join, 39.0 before the K loop).  Those of up to 20 read it at once behind the loop (4096 x
+// 2112 x 7168 with all terms: 90.2 us, 96.9 a row ahead).  The 256 x 256 tile's 32
 // fragments leave registers for two rows of the residual, which is read a row ahead
 // (4096 x 4096 x 7168 with UE8M0 scales and all terms: 121 us, 126 at once, 122 two rows
 // ahead; 115 with 16-byte accesses).
@@ -1294,6 +1295,13 @@ __global__ __launch_bounds__(T::kThreads) void gemm_kernel(GemmParams p, Schedul
 #pragma unroll
           for (int i = 0; i < T::FM; ++i) {
             const int row = m0 + wm * T::TM + i * 16 + fr;
+            if constexpr (kEpilogue) {  // two fragments at a time
+              uint2 v[T::FN];
+#pragma unroll
+              for (int j = 0; j < T::FN; ++j) v[j] = make_uint2(packed[i][j][0], packed[i][j][1]);
+              FragmentRow<T>::store(D + (int64_t)row * p.ldd, row < rows_valid, n0 + wn * T::TN + 4 * kg, p.n, v);
+              continue;
+            }
             if (row >= rows_valid) continue;
             uint16_t* drow = D + (int64_t)row * p.ldd;
 #pragma unroll
