@@ -1,9 +1,9 @@
 // Gradient of a product's epilogue for gfx950: what reaches the sum, as the codes
 // that the input-gradient and the weight-gradient products take, and the bias'
-// gradient.  16384 x 4096 with the GELU, 414 MB: 95 us, 4.3 TB/s; bound by the vector
+// gradient.  16384 x 4096 with the GELU, 407 MB: 91.5 us, 4.5 TB/s; bound by the vector
 // units and the memory together (the slope, two quotients and two roundings for each
-// value).  With quotients from the hardware's reciprocal alone it takes 92 us, and codes
-// next to a boundary then fall on its wrong side.
+// value).  Quotients from the hardware's reciprocal alone save 3 us, and codes next to a
+// boundary then fall on its wrong side.
 
 #include "dg_act.h"
 #include "dg_block_internal.h"
