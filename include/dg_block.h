@@ -210,7 +210,8 @@ int dg_fp8_gemm_nt_ue8m0_epilogue(const uint8_t* a, const uint8_t* sfa, const ui
 /*
  * Gradient of the epilogue, from the gradient dd of d and the z that the
  * forward pass kept (the gradient of the residual is dd itself):
- *   dz = dd * act'(z)   (float32; act'(0) = 0 for the relu)
+ *   dz = dd * act'(z)   (float32; act'(0) = 0 for the relu; act' of a NaN is
+ *                        NaN, of an infinite z its limit, 0 or 1)
  * returned as
  *   dq  [rows][cols], dsf [cols/128][ld_dsf]: 1x128 codes, rows of the
  *       input-gradient GEMM; entries of dsf past the last row are not written

@@ -1,0 +1,82 @@
+"""GPU epilogue of the dense GEMM and its gradient where values are not finite: NaN and
+infinities of z, dd and the bias show where dg_block.h says, and nowhere else.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block
+from synth import bf16_normal
+from tests.block_util import check_f32, code_buffers, workspace
+from tests.gpu_util import bf16_to_f64, dev, host, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["none", "relu", "silu", "gelu_tanh"]
+NAN, QUIET, INF, MINUS_INF = 0x7FC0, 0xFFC1, 0x7F80, 0xFF80
+
+
+def gradient(dg, dd, z, act):
+    """(dq, dsf, dqt, dsft, dbias) on the host."""
+    rows, cols = dd.shape
+    dq, dsf = code_buffers(rows, cols, (rows + 3) // 4 * 4)
+    tiles = -(-rows // 128)
+    dqt, dsft = torch.zeros(cols, tiles * 128, dtype=torch.uint8, device="cuda"), torch.zeros(tiles, cols, device="cuda")
+    db = torch.zeros(cols, device="cuda")
+    dg.dg_epilogue_bwd(dev(dd), dq, dsf, pre=None if act == "none" else dev(z), act=act, dqt=dqt, dsft=dsft, dbias=db,
+                       workspace=workspace(dg.dg_get_epilogue_bwd_workspace_size(rows, cols)))
+    return [host(t) for t in (dq, dsf, dqt, dsft, db)]
+
+
+def same_but_for(got, want, rows, cols):
+    """Everything as in `want` but the codes' tiles and columns that the given values belong to."""
+    keep_r = np.ones(len(want[0]), bool)
+    keep_r[rows] = False
+    keep_c = np.ones(want[0].shape[1], bool)
+    keep_c[cols] = False
+    assert np.array_equal(got[0][keep_r], want[0][keep_r]) and np.array_equal(got[1][:, :len(keep_r)][:, keep_r], want[1][:, :len(keep_r)][:, keep_r])
+    assert np.array_equal(got[2][keep_c], want[2][keep_c]) and np.array_equal(got[3][:, keep_c], want[3][:, keep_c])
+    assert np.array_equal(got[4][keep_c], want[4][keep_c])
+
+
+@pytest.mark.parametrize("rows", [100, 200])
+@pytest.mark.parametrize("act", ACTS)
+def test_nan_shows_in_its_column_of_dbias(rows, act):
+    """A NaN of z or of dd, of either sign, in one and in several tiles of rows."""
+    dg = require_gpu()
+    dd, z = bf16_normal((rows, 384), 1), bf16_normal((rows, 384), 2, 2.0)
+    want = gradient(dg, dd, z, act)
+    at_rows, at_cols = [5, rows - 1, 70], [7, 200, 383]
+    for where in (("dd", "z") if act != "none" else ("dd",)):
+        bad = {"dd": dd.copy(), "z": z.copy()}
+        bad[where][at_rows, at_cols] = [NAN, QUIET, NAN]
+        got = gradient(dg, bad["dd"], bad["z"], act)
+        assert np.flatnonzero(np.isnan(got[4])).tolist() == at_cols, where
+        same_but_for(got, want, at_rows, at_cols)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu_tanh"])
+def test_infinite_z_has_the_slopes_limit(act):
+    dg = require_gpu()
+    dd, z = bf16_normal((140, 256), 3), bf16_normal((140, 256), 4, 2.0)
+    far = z.copy()
+    z[[3, 130], [10, 11]], far[[3, 130], [10, 11]] = [INF, MINUS_INF], [0x7149, 0xF149]  # +-1e30
+    got = gradient(dg, dd, z, act)
+    for u, v in zip(got, gradient(dg, dd, far, act)):
+        assert np.array_equal(u, v)
+    v = bf16_to_f64(dd) * block.act_slope(bf16_to_f64(far), act)
+    check_f32(torch.as_tensor(got[4]), v.sum(0), np.abs(v).sum(0) + np.abs(bf16_to_f64(dd)).sum(0), "dbias")
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_nan_of_a_bias_shows_in_its_column(act):
+    dg = require_gpu()
+    m, n = 70, 136
+    a, b = torch.zeros(m, 128, dtype=torch.uint8, device="cuda"), torch.zeros(n, 128, dtype=torch.uint8, device="cuda")
+    bias = torch.ones(n, device="cuda")
+    bias[9], bias[135] = float("nan"), -float("nan")
+    d, z = (torch.zeros(m, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dg.dg_fp8_gemm_nt_epilogue(a, torch.zeros(1, 72, device="cuda"), b, torch.zeros(2, 1, device="cuda"), d, bias=bias, act=act, pre=z)
+    nan = bias.isnan().expand(m, n)
+    assert torch.equal(d.isnan(), nan) and torch.equal(z.isnan(), nan)
