@@ -15,6 +15,7 @@
 #include "dg_math.h"
 #include "dg_moe_internal.h"
 #include "dg_route_rows.h"
+#include "dg_turns.h"
 
 namespace dg {
 namespace {
@@ -189,14 +190,15 @@ __global__ __launch_bounds__(64 * kSumWaves) void balance_kernel(BalanceParams p
       fetch_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, next);
       if (lane < p.topk) next_id = p.ids[(int64_t)t * p.topk + lane];
     };
-    if (from + wave < to) fetch(from + wave);
+    Turns<kSumWaves> turn(from, to, wave);
+    if (turn.here()) fetch(turn.row());
     __syncthreads();
-    for (int t = from + wave; t < to; t += kSumWaves) {
+    for (; turn.here(); turn.next()) {
       float x[V], share[V], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = next[i];
       const int id = next_id;
-      if (t + kSumWaves < to) fetch(t + kSumWaves);
+      if (turn.has_next()) fetch(turn.next_row());
       arrange_row<VEC>(lane, sums[wave], x);
       float inv = 1.0f;
       if (ordinary<V>(x, p.sigmoid != 0, top)) {
@@ -324,7 +326,8 @@ __global__ __launch_bounds__(64 * kWaves) void balance_bwd_kernel(BalanceParams 
       const int e = lane * V + i;
       f[i] = e < p.experts ? per * (float)p.counts[(int64_t)s * p.experts + e] : 0.0f;
     }
-    for (int t = from + wave; t < to; t += kWaves) {
+    for (Turns<kWaves> turn(from, to, wave); turn.here(); turn.next()) {
+      const int t = turn.row();
       float x[V], add[V], share[V], g[V], top = 0.0f;
       load_row<VEC>(static_cast<const T*>(p.logits) + (int64_t)t * p.ld, p.experts, lane, rows[wave], x);
       if (p.add) load_row<VEC>(static_cast<const T*>(p.add) + (int64_t)t * p.ld_add, p.experts, lane, rows[wave], add);
