@@ -83,14 +83,15 @@ const char* layout_name(int layout) {
 }
 
 // Shared checks for the three GEMM entry points.  rows = the rows of the
-// layout's row space (M, M_total or M_max).
+// layout's row space (M, M_total or M_max).  nothing: a call without output
+// values that may give null for matrices that have none.
 int check_gemm_common(const uint8_t* a, const void* sfa, const uint8_t* b, const void* sfb,
                       const uint16_t* d, int rows, int n, int k, int64_t lda, int64_t ldb,
-                      int64_t ldd, int64_t ld_sfa) {
+                      int64_t ldd, int64_t ld_sfa, bool nothing = false) {
   if (rows < 0 || n < 0 || k < 0) return fail(DG_ERR_INVALID_VALUE, "negative dimension (m=%d n=%d k=%d)", rows, n, k);
   if (k % 128 != 0) return fail(DG_ERR_UNSUPPORTED_SHAPE, "k=%d is not a multiple of 128", k);
   // With k == 0 nothing of A, B or the scales is read, so only d must be valid.
-  if (!d || (k > 0 && (!a || !sfa || !b || !sfb)))
+  if (!nothing && (!d || (k > 0 && (!a || !sfa || !b || !sfb))))
     return fail(DG_ERR_INVALID_VALUE, "null pointer argument");
   if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned16(sfa) || !aligned16(sfb))
     return fail(DG_ERR_MISALIGNED, "a, b, d, sfa and sfb must be 16-byte aligned");
@@ -98,7 +99,8 @@ int check_gemm_common(const uint8_t* a, const void* sfa, const uint8_t* b, const
   if (ldd < n) return fail(DG_ERR_INVALID_VALUE, "ldd smaller than n");
   if (lda % 16 || ldb % 16) return fail(DG_ERR_MISALIGNED, "lda and ldb must be multiples of 16 bytes");
   if (ldd % 8) return fail(DG_ERR_MISALIGNED, "ldd must be a multiple of 8 elements");
-  if (ld_sfa < rows || ld_sfa < 4) return fail(DG_ERR_INVALID_VALUE, "ld_sfa=%lld smaller than rows (%d) or 4", (long long)ld_sfa, rows);
+  if (ld_sfa < rows || (!nothing && ld_sfa < 4))
+    return fail(DG_ERR_INVALID_VALUE, "ld_sfa=%lld smaller than rows (%d) or 4", (long long)ld_sfa, rows);
   if (ld_sfa % 4) return fail(DG_ERR_MISALIGNED, "ld_sfa must be a multiple of 4");
   // The kernels address each operand (per group) with 32-bit byte offsets.
   const int64_t lim = (int64_t)1 << 32;
@@ -160,12 +162,12 @@ struct QOut {
 };
 
 // Checks of the quantised-output arguments; rows = the rows of one group.
-int check_qout(const QOut* q, int rows, int n, int groups) {
+int check_qout(const QOut* q, int rows, int n, int groups, bool nothing = false) {
   if (!q) return DG_SUCCESS;
-  if (!q->dq || !q->dsf) return fail(DG_ERR_INVALID_VALUE, "null dq or dsf");
+  if (!nothing && (!q->dq || !q->dsf)) return fail(DG_ERR_INVALID_VALUE, "null dq or dsf");
   if (!aligned16(q->dq) || !aligned16(q->dsf)) return fail(DG_ERR_MISALIGNED, "dq and dsf must be 16-byte aligned");
   if (n % 128) return fail(DG_ERR_UNSUPPORTED_SHAPE, "n=%d is not a multiple of 128 (quantised output)", n);
-  if (q->ld_dsf < rows || q->ld_dsf < 4) return fail(DG_ERR_INVALID_VALUE, "ld_dsf smaller than the rows or 4");
+  if (q->ld_dsf < rows || (!nothing && q->ld_dsf < 4)) return fail(DG_ERR_INVALID_VALUE, "ld_dsf smaller than the rows or 4");
   if (q->ld_dsf % 4) return fail(DG_ERR_MISALIGNED, "ld_dsf must be a multiple of 4");
   if ((int64_t)rows * n > (((int64_t)1 << 40) - 1) / groups) return fail(DG_ERR_UNSUPPORTED_SHAPE, "quantised output too large");
   if (!below((int64_t)groups * (n / 128), q->ld_dsf, 4, (int64_t)1 << 40))
@@ -210,10 +212,10 @@ int gemm_nt_impl(const uint8_t* a, const void* sfa, const uint8_t* b, const void
                  int m, int n, int k, int64_t lda, int64_t ldb, int64_t ldd, int64_t ld_sfa,
                  void* workspace, size_t workspace_bytes, void* stream, bool ue8m0,
                  const QOut* qo = nullptr, const dg::GemmEpilogue* epi = nullptr) {
-  // An empty output of a caller's allocator may have no address.
-  if (epi && (m == 0 || n == 0) && m >= 0 && n >= 0 && k >= 0 && k % 128 == 0) return ok();
-  int st = check_gemm_common(a, sfa, b, sfb, d, m, n, k, lda, ldb, ldd, ld_sfa);
-  if (st == DG_SUCCESS) st = check_qout(qo, m, n, 1);
+  // Empty matrices of a caller's allocator may have no address.
+  const bool nothing = epi && (m == 0 || n == 0);
+  int st = check_gemm_common(a, sfa, b, sfb, d, m, n, k, lda, ldb, ldd, ld_sfa, nothing);
+  if (st == DG_SUCCESS) st = check_qout(qo, m, n, 1, nothing);
   if (st == DG_SUCCESS && epi) st = check_epilogue(*epi, m, n);
   if (st != DG_SUCCESS) return st;
   if (m == 0 || n == 0) return ok();
