@@ -75,22 +75,24 @@ int norm_impl(const uint16_t* y, const uint16_t* h, const float* gate, const flo
               const float* bias, uint16_t* r, uint16_t* x, uint8_t* q, void* sf, int tokens, int cols, int64_t ld_y,
               int64_t ld_h, int64_t ld_r, int64_t ld_x, int64_t ld_sf, int kind, int post, int gate_kind,
               float res_scale, float eps, void* stream, bool pow2) {
-  if (!q != !sf) return fail(DG_ERR_INVALID_VALUE, "q and sf go together");
-  DG_TRY(check_norm(tokens, cols, q ? 128 : 8, kind, gate_kind, gate, eps));
+  const bool codes = q || sf;
+  DG_TRY(check_norm(tokens, cols, codes ? 128 : 8, kind, gate_kind, gate, eps));
   if (post_weight && !post) return fail(DG_ERR_INVALID_VALUE, "post_weight without post");
-  if ((weight || bias) && !x && !q) return fail(DG_ERR_INVALID_VALUE, "weight or bias without x or q");
+  // Matrices without rows may be null, parameters and scales beside them are not.
+  if (tokens > 0 && !q != !sf) return fail(DG_ERR_INVALID_VALUE, "q and sf go together");
+  if (tokens > 0 && (weight || bias) && !x && !q) return fail(DG_ERR_INVALID_VALUE, "weight or bias without x or q");
   DG_TRY(check_ld("ld_y", ld_y, cols, 8, tokens, 2));
   if (h) DG_TRY(check_ld("ld_h", ld_h, cols, 8, tokens, 2));
   if (r) DG_TRY(check_ld("ld_r", ld_r, cols, 8, tokens, 2));
   if (x) DG_TRY(check_ld("ld_x", ld_x, cols, 8, tokens, 2));
-  if (q) DG_TRY(check_ld("ld_sf", ld_sf, tokens, 4, cols / 128, 4));
+  if (codes) DG_TRY(check_ld("ld_sf", ld_sf, tokens, 4, cols / 128, 4));
   if (r && r == h && ld_r != ld_h) return fail(DG_ERR_INVALID_VALUE, "r in place of h needs ld_r == ld_h");
-  if (tokens == 0) return ok();
-  if (!y) return fail(DG_ERR_INVALID_VALUE, "null y");
-  if (!r && !x && !q) return fail(DG_ERR_INVALID_VALUE, "no result is wanted");
+  if (tokens > 0 && !y) return fail(DG_ERR_INVALID_VALUE, "null y");
+  if (tokens > 0 && !r && !x && !q) return fail(DG_ERR_INVALID_VALUE, "no result is wanted");
   for (const void* ptr : {(const void*)y, (const void*)h, (const void*)post_weight, (const void*)weight, (const void*)bias,
                           (const void*)r, (const void*)x, (const void*)q, (const void*)sf})
     if (!aligned16(ptr)) return fail(DG_ERR_MISALIGNED, "data pointers and [cols] parameters must be 16-byte aligned");
+  if (tokens == 0) return ok();
   const dg::NormParams p{y,      h,    gate, post_weight, weight, bias, r,     x,                     q,    sf,        tokens,
                          cols,   ld_y, ld_h, ld_r,        ld_x,   ld_sf, kind == DG_NORM_LAYER, post != 0, gate_kind, res_scale, eps};
   return launched(dg::launch_block_norm(p, pow2, static_cast<hipStream_t>(stream)), "block_norm");

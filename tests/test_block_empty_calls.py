@@ -37,3 +37,18 @@ def test_gemm_of_nothing_needs_no_addresses(name):
     assert call(name, m=0, ld_sfa=0, ld_dsf=0, **nulls) == 0
     assert call(name, n=0, b=0, sfb=0, d=0, residual=0, pre=0, dq=0, dsf=0, bias=0) == 0
     assert call(name, m=0, n=0, ld_sfa=0, ld_dsf=0, b=0, sfb=0, bias=0, dsf=0, **nulls) == 0
+
+
+@pytest.mark.parametrize("name", ["dg_block_norm", "dg_block_norm_ue8m0"])
+def test_norm_of_no_tokens_needs_no_addresses(name):
+    """What a caller's allocator gives for [0][cols] matrices is null, for scales [cols/128][ld] it is not."""
+    nothing = dict(tokens=0, y=0, h=0, r=0, x=0, q=0, gate=0)
+    assert call(name, **nothing) == 0
+    assert call(name, **{**nothing, "gate_kind": 2}) == 0
+    assert call(name, **nothing, sf=0) == 0
+    assert call(name, **nothing, ld_sf=0) == 0
+    # The rest is checked as in any call.
+    assert call(name, **nothing, kind=2) == INVALID and call(name, **nothing, eps=0.0) == INVALID
+    assert call(name, **nothing, cols=520, ld_y=520) == SHAPE and call(name, **nothing, ld_sf=66) == MISALIGNED
+    assert call(name, **nothing, post=0) == INVALID and call(name, tokens=0, y=FAKE + 8) == MISALIGNED
+    assert call(name, **nothing, ld_y=504) == INVALID and call(name, **nothing, weight=FAKE + 4) == MISALIGNED
