@@ -48,7 +48,7 @@ __device__ __forceinline__ float inverse_root(float a) {
 template <int TEAM>
 struct TeamSums {
   static constexpr int kWaves = TEAM > 64 ? TEAM / 64 : 1;
-  float words[2][kWaves][4];
+  float words[2][kWaves][5];
 };
 
 template <int TEAM, int N>
@@ -112,32 +112,56 @@ __device__ __forceinline__ void times_columns(const float* w, const Chunks<TEAM,
   }
 }
 
-// What norm(v) multiplies v by; a layer norm's mean is taken off v here.  It takes
-// the mean first and the squares of what is left: a single pass would lose rows with a
-// large mean.
-template <int TEAM, int V>
-__device__ __forceinline__ float norm_scale(float (&v)[V][8], const Chunks<TEAM, V>& c, bool layer, float inv_cols, float eps,
-                                            TeamSums<TEAM>& lds, int& turn) {
-  if (layer) {
+// A layer norm takes the mean first and the squares of what is left, since a single pass
+// would lose rows with a large mean.  What the roundings of the sum leave of the mean,
+// the mean of what is left, comes with the squares: rows whose values hardly differ would
+// keep it in every value (7168 times 1000: 2^-14, which the root of eps makes 0.06).
+//   sum (v - m)^2 of what is left with its mean m = sum v^2 - m sum v
+__device__ __forceinline__ float squares_around(float squares, float sum, float mean) {
+  return fmaxf(fmaf(-sum, mean, squares), 0.0f);
+}
+
+// norm(v) = scale v + shift.  A layer norm's mean is taken off v here, and what that
+// leaves of it is the shift.
+struct Affine {
+  float scale, shift;
+};
+template <bool LAYER, int TEAM, int V>
+__device__ __forceinline__ Affine norm_of(float (&v)[V][8], const Chunks<TEAM, V>& c, float inv_cols, float eps,
+                                          TeamSums<TEAM>& lds, int& turn) {
+  if constexpr (LAYER) {
     float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += v[i][e];
     team_sums<TEAM>(sum, lds, turn);
-    const float mean = sum[0] * inv_cols;
+    const float mean = sum[0] / (float)(c.count * 8);
+    float s[2] = {0.0f, 0.0f};  // squares, sum of what is left
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = c.in(i) ? v[i][e] - mean : 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        const float d = c.in(i) ? v[i][e] - mean : 0.0f;
+        v[i][e] = d, s[0] = fmaf(d, d, s[0]), s[1] += d;
+      }
+    team_sums<TEAM>(s, lds, turn);
+    const float rest = s[1] * inv_cols;
+    const float scale = inverse_root(fmaf(squares_around(s[0], s[1], rest), inv_cols, eps));
+    return {scale, -rest * scale};
+  } else {
+    float squares[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) squares[0] = fmaf(v[i][e], v[i][e], squares[0]);
+    team_sums<TEAM>(squares, lds, turn);
+    return {inverse_root(fmaf(squares[0], inv_cols, eps)), 0.0f};
   }
-  float squares[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) squares[0] = fmaf(v[i][e], v[i][e], squares[0]);
-  team_sums<TEAM>(squares, lds, turn);
-  return inverse_root(fmaf(squares[0], inv_cols, eps));
+}
+template <bool LAYER>
+__device__ __forceinline__ float normed(float v, const Affine& n) {
+  return LAYER ? fmaf(v, n.scale, n.shift) : v * n.scale;
 }
 
 // Codes of 8 values x + rest (rest: what the rounding of x left), a tile of 128 by 16
@@ -185,7 +209,7 @@ template <int TEAM>
 constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 
 // Bound by the memory: everything is read once and written once (16384 x 7168 with both
-// norms, gate, r and codes: 207 us, 5.1 TB/s, where a copy of 256 MiB reaches 5.2; one
+// norms, gate, r and codes: 205 us, 5.2 TB/s, where a copy of 256 MiB reaches 5.2; one
 // row: 3.6 us, the launch).  The teams are the smallest that hold a row in 16 values a
 // thread, since a row's sums wait for its last load and other rows have to fill that
 // time: 512 threads for 7168 columns 207 us, 256 threads of 32 values 216, 1024 of 8
@@ -193,7 +217,7 @@ constexpr int kBwdThreads = TEAM < 256 ? 512 : TEAM;
 // STREAMING: results larger than the L2s, which nothing reads back through them
 // (store_streaming; 4096 x 7168 with r, bf16 rows and codes: 49.0 us, and 54.5 with
 // plain stores).
-template <bool POW2, bool STREAMING, int TEAM, int V>
+template <bool POW2, bool STREAMING, bool LAYER, int TEAM, int V>
 __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) {
   constexpr int kTeams = kNormThreads<TEAM> / TEAM;
   static_assert(kTeams == 1 || TEAM <= 64, "teams that share a workgroup need no barrier");
@@ -210,11 +234,11 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
 #pragma unroll
     for (int i = 0; i < V; ++i) widen8(y[i], v[i]);
     if (p.post) {
-      const float k = norm_scale(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
+      const Affine n = norm_of<LAYER>(v, c, inv_cols, p.eps, lds, turn);
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= k;
+        for (int e = 0; e < 8; ++e) v[i][e] = !LAYER || c.in(i) ? normed<LAYER>(v[i][e], n) : 0.0f;
       times_columns(p.post_weight, c, v);
     }
     if (p.gate_kind == DG_GATE_COLUMN) {
@@ -241,7 +265,7 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
         if (c.in(i)) store8<STREAMING>(p.r + t * p.ld_r + c.at(i) * 8, v[i]);
     }
     if (!p.x && !p.q) continue;
-    const float k = norm_scale(v, c, p.layer != 0, inv_cols, p.eps, lds, turn);
+    const Affine norm = norm_of<LAYER>(v, c, inv_cols, p.eps, lds, turn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = c.at(i);
@@ -254,9 +278,9 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float n = v[i][e] * k;
+        const float n = normed<LAYER>(v[i][e], norm), of_n = fmaf(v[i][e], norm.scale, -n);
         x[e] = n * w[e];
-        rest[e] = fmaf(fmaf(v[i][e], k, -n), w[e], fmaf(n, w[e], -x[e]));
+        rest[e] = fmaf(LAYER ? of_n + norm.shift : of_n, w[e], fmaf(n, w[e], -x[e]));
       }
       if (p.bias && c.in(i)) {
         float b[8];
@@ -429,7 +453,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
       load_raw(p, t, read_y, c, raw);
     }
     // The sums that both norms' statistics need, together: the mean first (layer),
-    // then squares and products with what is left.
+    // then squares and products with what is left, and its own mean (squares_around).
     float mean_r = 0.0f, mean_y = 0.0f, mean_g = 0.0f;
     if constexpr (LAYER) {
       float s[3] = {0.0f, 0.0f, 0.0f};
@@ -450,9 +474,10 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         }
       }
       team_sums<TEAM>(s, lds, turn);
-      mean_r = s[0] * inv_cols, mean_y = s[1] * inv_cols, mean_g = s[2] * inv_cols;
+      mean_r = s[0] / (float)p.cols, mean_y = s[1] / (float)p.cols, mean_g = s[2] * inv_cols;
     }
-    float s[3] = {0.0f, 0.0f, 0.0f};  // squares of r, products of g and r, squares of y
+    // Squares of r, products of g and r, squares of y; sums of what is left of r and y.
+    float s[LAYER ? 5 : 3] = {};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!c.in(i)) continue;
@@ -466,6 +491,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
           const float d = a[e] - mean_r;
           s[0] = fmaf(d, d, s[0]);
           s[1] = fmaf(b[e] * w[e], d, s[1]);
+          if constexpr (LAYER) s[3] += d;
         }
       }
       if (POST) {
@@ -474,13 +500,21 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         for (int e = 0; e < 8; ++e) {
           const float d = a[e] - mean_y;
           s[2] = fmaf(d, d, s[2]);
+          if constexpr (LAYER) s[4] += d;
         }
       }
     }
     if (p.dx || POST) team_sums<TEAM>(s, lds, turn);
+    float rest_r = 0.0f, rest_y = 0.0f;
+    if constexpr (LAYER) {
+      rest_r = s[3] * inv_cols, rest_y = s[4] * inv_cols;
+      s[0] = squares_around(s[0], s[3], rest_r), s[2] = squares_around(s[2], s[4], rest_y);
+      s[1] = fmaf(-mean_g, s[3], s[1]);  // rest_r times the sum of g
+    }
     const float kr = inverse_root(fmaf(s[0], inv_cols, p.eps));
     const float ky = POST ? inverse_root(fmaf(s[2], inv_cols, p.eps)) : 1.0f;
     const float gn = s[1] * inv_cols * kr;  // mean of g n
+    const float shift_r = -rest_r * kr, shift_y = -rest_y * ky;  // norm(v) = (v - mean) k + shift
     const float token_gate = p.gate_kind == DG_GATE_TOKEN ? p.gate[t] : 1.0f;
     float tot[V][8];  // t, then e
     float after[3] = {0.0f, 0.0f, 0.0f};  // sums of e post_weight, of that times n(y), of t u
@@ -499,7 +533,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         weight.get(c, i, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          n[e] = (n[e] - mean_r) * kr;
+          n[e] = fmaf(n[e] - mean_r, kr, shift_r);
           if constexpr (EXTRA) db.kept[i][e] += b[e];
           tot[i][e] = fmaf(kr, fmaf(-n[e], gn, fmaf(b[e], w[e], -mean_g)), tot[i][e]);
         }
@@ -518,7 +552,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         widen8(raw.y[i], yv);
         if (POST) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) yv[e] = (yv[e] - mean_y) * ky;
+          for (int e = 0; e < 8; ++e) yv[e] = fmaf(yv[e] - mean_y, ky, shift_y);
         }
         if (p.dgate) {
 #pragma unroll
@@ -551,7 +585,7 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         widen8(raw.y[i], yv);
         const float m = LAYER ? after[0] * inv_cols : 0.0f, mn = after[1] * inv_cols;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tot[i][e] = ky * fmaf(-(yv[e] - mean_y) * ky, mn, tot[i][e] - m);
+        for (int e = 0; e < 8; ++e) tot[i][e] = ky * fmaf(-fmaf(yv[e] - mean_y, ky, shift_y), mn, tot[i][e] - m);
       }
       store8<true>(p.dy + t * p.ld_dy + c.at(i) * 8, tot[i]);
     }
@@ -631,7 +665,8 @@ void go_norm(const NormParams& p, hipStream_t stream) {
   constexpr int kTeams = kNormThreads<TEAM> / TEAM;
   const int64_t need = ((int64_t)p.tokens + kTeams - 1) / kTeams;
   const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
-  hipLaunchKernelGGL((norm_kernel<POW2, STREAMING, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
+  if (p.layer) hipLaunchKernelGGL((norm_kernel<POW2, STREAMING, true, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
+  else hipLaunchKernelGGL((norm_kernel<POW2, STREAMING, false, TEAM, V>), dim3(grid), dim3(kNormThreads<TEAM>), 0, stream, p);
 }
 
 template <bool POW2, bool STREAMING>
