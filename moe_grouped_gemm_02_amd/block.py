@@ -9,7 +9,7 @@ are also available from the package itself.
 
 Tensor conventions are those of the mixture-of-experts operators: codes may be
 torch.uint8 or torch.float8_e4m3fn, UE8M0 scales torch.uint8 or
-torch.float8_e8m0fnu.
+torch.float8_e8m0fnu.  All tensors of a call are on the current device.
 """
 
 import ctypes
@@ -17,7 +17,7 @@ import ctypes
 import torch
 
 from . import _BF, _I, _L, _P, _S, _U8, _check, _expect, _lib, _sfb_shape
-from .moe import (_E8, _F32, _I32, _dense, _dense_or_none, _int, _matrix, _scales, _score, _shape, _stream, _topk,
+from .moe import (_E8, _F32, _I32, _dense, _dense_or_none, _int, _matrix, _raw_stream, _scales, _score, _shape, _topk,
                   _workspace)
 
 _F = ctypes.c_float
@@ -56,6 +56,31 @@ def _choice(table, value, name):
         raise ValueError(f"{name} must be one of {sorted(table)}, not {value!r}") from None
 
 
+# The current device's index: torch.cuda.current_device() without its check that
+# CUDA has been initialised, which the tensors answer.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_several = None  # whether there is more than one device, once a call has asked
+
+
+def _stream(lead, *others):
+    """Handle of the current stream of the device that the tensors are on, which must be
+    the current one.  The launch goes to the current device, whatever device the default
+    stream's handle (0) was taken from, and a kernel may fault on another device's
+    addresses.  (Where a process sees one device there is nothing to ask: 0.1 us a
+    tensor of a call that has 8 us in all.)"""
+    global _several
+    index = lead.get_device()
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several:
+        if index != _current_device():
+            raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"a tensor on {t.device} beside those on cuda:{index}")
+    return _raw_stream(index)
+
+
 def _rows(t, name, rows, cols):
     """Address and row stride of a bf16 matrix of the given shape, or of none."""
     if t is None:
@@ -92,7 +117,7 @@ def _block_norm(fn, sf_dtypes, y, h, r, x, q, sf, weight, bias, post, post_weigh
         y_at, h_at, gate_at, _dense_or_none(post_weight, "post_weight", _F32, shape),
         _dense_or_none(weight, "weight", _F32, shape), _dense_or_none(bias, "bias", _F32, shape), r_at, x_at, q_at, sf_at,
         tokens, cols, ld_y, ld_h, ld_r, ld_x, ld_sf, _choice(_KINDS, kind, "kind"), bool(post), gate_kind, res_scale, eps,
-        _stream(y)))
+        _stream(y, h, r, x, q, sf, weight, bias, post_weight, gate)))
     return r, x, q, sf
 
 
@@ -143,7 +168,8 @@ def dg_block_norm_bwd(dy, dx=None, dr=None, r=None, y=None, dh=None, weight=None
         _dense_or_none(weight, "weight", _F32, shape), dy_at, dh_at, _dense_or_none(dweight, "dweight", _F32, shape),
         _dense_or_none(dbias, "dbias", _F32, shape), _dense_or_none(dpost_weight, "dpost_weight", _F32, shape), dgate_at,
         tokens, cols, ld_dx, ld_dr, ld_r, ld_y, ld_dy, ld_dh, _choice(_KINDS, kind, "kind"), bool(post), gate_kind, res_scale,
-        eps, *_workspace(workspace), _stream(dy)))
+        eps, *_workspace(workspace),
+        _stream(dy, dx, dr, r, y, dh, weight, dweight, dbias, post_weight, dpost_weight, gate, dgate, workspace)))
     return dy, dh, dweight, dbias, dpost_weight, dgate
 
 
@@ -170,7 +196,7 @@ def _balance(fn, dtypes, logits, ids, counts, used, loss, seq_offsets, score, co
     _check(fn, _FUNCTIONS[fn](
         logits_at, ids_at, offsets_at, _dense(counts, "counts", _I32, (seqs, experts)), _dense(used, "used", _I32, (seqs,)),
         _dense(loss, "loss", _F32, (1,)), tokens, experts, topk, seqs, ld, _score(score), coef, *_workspace(workspace),
-        _stream(logits)))
+        _stream(logits, ids, counts, used, loss, seq_offsets, workspace)))
     return counts, used, loss
 
 
@@ -201,7 +227,7 @@ def _balance_bwd(fn, dtypes, logits, counts, used, dlogits, topk, seq_offsets, d
     _check(fn, _FUNCTIONS[fn](
         logits_at, _dense(counts, "counts", _I32, (seqs, experts)), _dense(used, "used", _I32, (seqs,)), offsets_at,
         _dense_or_none(dloss, "dloss", _F32, (1,)), add_at, dlogits_at, tokens, experts, _int(topk, "topk"), seqs, ld, ld_add,
-        ld_d, _score(score), coef, _stream(logits)))
+        ld_d, _score(score), coef, _stream(logits, counts, used, dlogits, seq_offsets, dloss, add)))
     return dlogits
 
 
@@ -250,7 +276,8 @@ def _gemm_epilogue(fn, ue8m0, a, sfa, b, sfb, d, bias, act, residual, pre, dq, d
         dsf_at, ld_dsf = _scales(dsf, "dsf", sf_dtypes, (n // 128,), m)
     _check(fn, _FUNCTIONS[fn](
         a_at, sfa_at, b_at, sfb_at, _dense_or_none(bias, "bias", _F32, (n,)), res_at, d_at, pre_at, dq_at, dsf_at, m, n, k, lda,
-        ldb, ldd, ld_sfa, ld_res, ld_pre, ld_dsf, _choice(_ACTS, act, "act"), *_workspace(workspace), _stream(d)))
+        ldb, ldd, ld_sfa, ld_res, ld_pre, ld_dsf, _choice(_ACTS, act, "act"), *_workspace(workspace),
+        _stream(d, a, sfa, b, sfb, bias, residual, pre, dq, dsf, workspace)))
     return d
 
 
@@ -291,7 +318,8 @@ def dg_epilogue_bwd(dd, dq, dsf, pre=None, act="none", dqt=None, dsft=None, dbia
         dsft_at, ld_dsft = _scales(dsft, "dsft", _F32, (tiles,), cols)
     _check("dg_epilogue_bwd", _lib.dg_epilogue_bwd(
         dd_at, pre_at, dq_at, dsf_at, dqt_at, dsft_at, _dense_or_none(dbias, "dbias", _F32, (cols,)), rows, cols, ld_dd, ld_pre,
-        ld_dsf, ld_dsft, _choice(_ACTS, act, "act"), *_workspace(workspace), _stream(dd)))
+        ld_dsf, ld_dsft, _choice(_ACTS, act, "act"), *_workspace(workspace),
+        _stream(dd, dq, dsf, pre, dqt, dsft, dbias, workspace)))
     return dq, dsf, dqt, dsft, dbias
 
 
