@@ -80,3 +80,22 @@ def test_nan_of_a_bias_shows_in_its_column(act):
     dg.dg_fp8_gemm_nt_epilogue(a, torch.zeros(1, 72, device="cuda"), b, torch.zeros(2, 1, device="cuda"), d, bias=bias, act=act, pre=z)
     nan = bias.isnan().expand(m, n)
     assert torch.equal(d.isnan(), nan) and torch.equal(z.isnan(), nan)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_activations_down_to_the_last_bf16_numbers(act):
+    """Where z / (1 + e^-t) leaves the range of bf16 (z = -88 to -98 for the SiLU, about -10 for the GELU), results are as
+    accurate as elsewhere: t is off by a few roundings, 2^-22 of up to 142 (powers of 2), which is 2^-14.6 of the result;
+    then one rounding, to half of 2^-133 at least."""
+    dg = require_gpu()
+    n = 4096
+    z = torch.cat([torch.linspace(-100, -80, n // 2, device="cuda"), torch.linspace(-12, -8, n // 2, device="cuda")])
+    d = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda")
+    a, b = torch.zeros(1, 0, dtype=torch.uint8, device="cuda"), torch.zeros(n, 0, dtype=torch.uint8, device="cuda")
+    dg.dg_fp8_gemm_nt_epilogue(a, torch.zeros(0, 4, device="cuda"), b, torch.zeros(32, 0, device="cuda"), d, bias=z, act=act)
+    want = block.act(z.double().cpu().numpy(), act)
+    got = d[0].double().cpu().numpy()
+    bad = ~(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -14.5) * np.abs(want) + 2.0 ** -134)
+    assert not bad.any(), f"{bad.sum()}, first at z = {float(z[int(np.flatnonzero(bad)[0])])}: {got[bad][0]} for {want[bad][0]}"
+    tiny = np.abs(want) < 2.0 ** -126  # some of them below the normal range
+    assert 10 < (tiny & (want < -2.0 ** -133)).sum()
