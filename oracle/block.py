@@ -65,10 +65,17 @@ def block_norm(y, h=None, weight=None, bias=None, post=False, post_weight=None, 
     return r, x, mag, xmag
 
 
+def _normed(v, kind, eps):
+    """norm(v), its magnitude and 1 / sqrt(..).  A mean is formed from terms of |v| / n: it can be off by what
+    float32 loses in their sum where v and the mean are next to 0 themselves (_norm counts that too)."""
+    mean, k = stats(v, kind, eps)
+    mag = np.abs(v) + np.abs(mean) + (np.abs(v).mean(1, keepdims=True) if kind == "layer" else 0.0)
+    return (v - mean) * k, mag * k, k
+
+
 def _norm_back(g, gmag, v, kind, eps):
     """Gradient of norm(v) from g, its magnitude, norm(v) and its magnitude."""
-    mean, k = stats(v, kind, eps)
-    n, nmag = (v - mean) * k, (np.abs(v) + np.abs(mean)) * k
+    n, nmag, k = _normed(v, kind, eps)
     d = g - n * (g * n).mean(1, keepdims=True)
     mag = gmag + nmag * (gmag * nmag).mean(1, keepdims=True)
     if kind == "layer":
@@ -97,16 +104,15 @@ def block_norm_bwd(dx=None, dr=None, r=None, y=None, weight=None, post=False, po
         y = _f64(y)
         u, umag = y, np.abs(y)
         if post:
-            mean, k = stats(y, kind, eps)
-            u, umag = (y - mean) * k * pw, (np.abs(y) + np.abs(mean)) * k * np.abs(pw)
+            n, nmag, _ = _normed(y, kind, eps)
+            u, umag = n * pw, nmag * np.abs(pw)
         if gate is not None:
             axis = 0 if np.ndim(gate) == 1 else 1
             keep = {} if axis == 0 else {"keepdims": True}
             out["dgate"] = (t * u).sum(axis, **keep), (tmag * umag).sum(axis, **keep)
     e, emag = (t, tmag) if gate is None else (t * _f64(gate), tmag * np.abs(_f64(gate)))
     if post:
-        mean, k = stats(y, kind, eps)
-        n, nmag = (y - mean) * k, (np.abs(y) + np.abs(mean)) * k
+        n, nmag, _ = _normed(y, kind, eps)
         out["dpost_weight"] = (e * n).sum(0), (emag * nmag).sum(0)
         e, emag, _, _ = _norm_back(e * pw, emag * np.abs(pw), y, kind, eps)
     out["dy"] = e, emag
