@@ -6,8 +6,9 @@ import pytest
 import torch
 
 from oracle import block
-from tests.block_util import code_buffers, f32, workspace
-from tests.gpu_util import require_gpu
+from tests.block_util import check_f32, check_rows, code_buffers, empty_rows, f32, padded, pads_kept, workspace
+from tests.gpu_util import bf16_to_f64, dev, host, require_gpu
+from tests.test_gpu_block_norm import BWD, parameters, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +112,67 @@ def test_layer_norm_gradient_of_flat_rows(cols, pad, post):
     near(dy, want["dy"][0], off, "dy")
     name = "dpost_weight" if post else "dweight"
     near(out, want[name][0], (size * (OFF + RELATIVE * n)).sum(0), name, 2.0 ** -24)
+
+
+# Forms of the gradient beside those of test_gpu_block_norm.py: two norms without the sums of a bias or of a column
+# gate, with a bias, and a column gate without a norm after the block.
+FORMS = {"post": (True, None, False), "post_token": (True, "token", False), "post_bias": (True, None, True), "post_all": (True, "column", True),
+         "column": (False, "column", False), "column_bias": (False, "column", True)}
+
+
+@pytest.mark.parametrize("tokens,cols,pad", [t for t in BWD if t[0]], ids=str)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("form", FORMS)
+def test_gradient_of_other_forms(tokens, cols, pad, kind, form):
+    dg = require_gpu()
+    post, gate, bias = FORMS[form]
+    dx, dr, r, y = (rows_of(tokens, cols, s) for s in (51, 52, 53, 54))
+    par = parameters(tokens, cols, 55, gate, False, post)
+    opts = dict(post=post, kind=kind, eps=1e-5, res_scale=float(np.float32(0.7)))
+    dev_par = {k: f32(v) for k, v in par.items()}
+    nans = lambda: torch.full((cols,), float("nan"), device="cuda")
+    out = {"dy": empty_rows(tokens, cols, pad), "dh": empty_rows(tokens, cols, pad), "dweight": nans()}
+    if bias:
+        out["dbias"] = nans()
+    if post:
+        out["dpost_weight"] = nans()
+    if gate:
+        out["dgate"] = torch.full_like(dev_par["gate"], float("nan"))
+    args = {k: padded(v, pad) for k, v in (("dx", dx), ("dr", dr), ("r", r), ("y", y))}
+    ws = workspace(dg.dg_get_block_norm_bwd_workspace_size(tokens, cols))
+    dg.dg_block_norm_bwd(workspace=ws, **args, **out, **dev_par, **opts)
+    want = block.block_norm_bwd(*(bf16_to_f64(v) for v in (dx, dr, r, y)), **par, **opts)
+    for name, got in out.items():
+        (check_rows if name in ("dy", "dh") else check_f32)(got, *want[name], name)
+    assert pads_kept(out["dy"]) and pads_kept(out["dh"])
+    again = {k: torch.zeros_like(v) for k, v in out.items()}
+    dg.dg_block_norm_bwd(workspace=workspace(ws.numel(), 0xFF), **args, **again, **dev_par, **opts)
+    for name in out:
+        assert torch.equal(again[name], out[name]), name
+
+
+@pytest.mark.parametrize("cols", [136, 512, 7168])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_nan_stays_in_its_row(cols, kind):
+    """Of the values, and of the gradient in its row and in the sums of its column."""
+    dg = require_gpu()
+    y, r, dx = (rows_of(5, cols, s) for s in (61, 62, 63))
+    opts = dict(post=True, kind=kind, eps=1e-5)
+
+    def run():
+        x, dy = empty_rows(5, cols), empty_rows(5, cols)
+        dg.dg_block_norm(dev(y), x=x, **opts)
+        dw, dpw = torch.zeros(cols, device="cuda"), torch.zeros(cols, device="cuda")
+        dg.dg_block_norm_bwd(dy, dx=dev(dx), r=dev(r), y=dev(y), dweight=dw, dpost_weight=dpw, **opts,
+                             workspace=workspace(dg.dg_get_block_norm_bwd_workspace_size(5, cols)))
+        return [t.clone() for t in (x, dy, dw, dpw)]
+
+    clean = run()
+    y[3, 7] = 0x7FC0
+    got = run()
+    keep = [0, 1, 2, 4]
+    assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][keep], clean[1][keep]) and torch.equal(got[2], clean[2])
+    assert np.isnan(bf16_to_f64(host(got[0])[3])).all() and np.isnan(bf16_to_f64(host(got[1])[3])).all() and bool(got[3].isnan().all())
+    y[3, 7], dx[1, 9] = 0x3F80, 0xFFC0
+    got = run()
+    assert np.isnan(bf16_to_f64(host(got[1])[1])).all() and bool(got[2].isnan()[9]) and int(got[2].isnan().sum()) == 1
