@@ -51,11 +51,11 @@ __device__ __forceinline__ float act_slope(float z) {
     const float slope = silu_slope(z, 1.0f, z, sigmoid(z));
     return z == z ? slope : z;  // the ranges that sigmoid() cuts take a NaN for a number
   } else if constexpr (ACT == DG_ACT_GELU_TANH) {
-    // Past +-9.5 the slope is 1 or below 2^-100; up to there t log2(e) lies in +-111, where
-    // the hardware's 2^x is in the normal range, and z^2 is finite.  log2(e) is part of the
-    // constants: two roundings of t, as without it, and none of a product with it (16384 x
-    // 4096: 91.5 us, and 95.5 with the exponent split off before).
-    const float v = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -9.5f), 9.5f), v2 = v * v;
+    // Up to +-10 t log2(e) lies in +-125.97, where the hardware's 2^x and its reciprocal are
+    // in the normal range and z^2 is finite; past that the slope is 1 or below 2^-117.
+    // log2(e) is part of the constants: two roundings of t, as without it, and none of a
+    // product with it (16384 x 4096: 91.5 us, and 95.5 with the exponent split off before).
+    const float v = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -10.0f), 10.0f), v2 = v * v;
     const float e = __builtin_amdgcn_exp2f(v * fmaf(kGelu3Log2e, v2, kGelu1Log2e));
     const float n = reciprocal(1.0f + e);  // 1 - sigmoid
     return e * n * fmaf(v * n, fmaf(3.0f * kGelu3, v2, kGelu1), 1.0f);

@@ -99,3 +99,20 @@ def test_activations_down_to_the_last_bf16_numbers(act):
     assert not bad.any(), f"{bad.sum()}, first at z = {float(z[int(np.flatnonzero(bad)[0])])}: {got[bad][0]} for {want[bad][0]}"
     tiny = np.abs(want) < 2.0 ** -126  # some of them below the normal range
     assert 10 < (tiny & (want < -2.0 ** -133)).sum()
+
+
+def test_gelu_slope_of_large_negative_z():
+    """One row, so that dbias is dd times the slope in float32: down to z = -10 within what t is off by (2^-23 of up to
+    126 powers of two, 2^-16, and as much again in the other factors), past that below 2^-117."""
+    dg = require_gpu()
+    z = np.concatenate([np.linspace(-10, -4, 384), np.linspace(-40, -10, 128)])
+    zt = torch.as_tensor(z, device="cuda").bfloat16()[None]
+    z = zt[0].double().cpu().numpy()
+    dd = torch.ones(1, 512, dtype=torch.bfloat16, device="cuda")
+    dq, dsf = code_buffers(1, 512, 4)
+    db = torch.zeros(512, device="cuda")
+    dg.dg_epilogue_bwd(dd, dq, dsf, pre=zt, act="gelu_tanh", dbias=db)
+    got, want = host(db).astype(np.float64), block.act_slope(z, "gelu_tanh")
+    near = z >= -10
+    assert near.sum() > 380 and np.all(np.abs(got - want)[near] <= 2.0 ** -15 * np.abs(want)[near])
+    assert np.all(np.abs(got[~near]) <= 2.0 ** -117)
