@@ -548,7 +548,9 @@ def _cpu_model():
 # reports it only while the sources are unchanged.
 
 PROFILES = os.path.join(os.path.dirname(os.path.abspath(__file__)), "profiles")
-KERNEL_SOURCES = ("dg_gemm.hip", "dg_gemm_kernel.h", "dg_device.h", "dg_internal.h")
+# dg_gemm.hip and the headers of csrc/ that it includes, directly or not.
+KERNEL_SOURCES = ("dg_gemm.hip", "dg_gemm_kernel.h", "dg_device.h", "dg_internal.h", "dg_act.h", "dg_math.h",
+                  "dg_moe_internal.h", "dg_tile.h")
 COPY_BYTES = 256 << 20
 
 
