@@ -48,7 +48,7 @@ __device__ __forceinline__ float inverse_root(float a) {
 template <int TEAM>
 struct TeamSums {
   static constexpr int kWaves = TEAM > 64 ? TEAM / 64 : 1;
-  float words[2][kWaves][5];
+  float words[2][kWaves][3];
 };
 
 template <int TEAM, int N>
@@ -113,10 +113,14 @@ __device__ __forceinline__ void times_columns(const float* w, const Chunks<TEAM,
 }
 
 // A layer norm takes the mean first and the squares of what is left, since a single pass
-// would lose rows with a large mean.  What the roundings of the sum leave of the mean,
-// the mean of what is left, comes with the squares: rows whose values hardly differ would
-// keep it in every value (7168 times 1000: 2^-14, which the root of eps makes 0.06).
-//   sum (v - m)^2 of what is left with its mean m = sum v^2 - m sum v
+// would lose rows with a large mean.  Of rows whose values hardly differ, the roundings of
+// the mean would stay in every value (7168 times 1000: 2^-14, which the root of eps makes
+// 0.06), so that what they leave of the mean, `rest`, is taken off too:
+// * bf16 values of two neighbouring powers of two are multiples of 2^-9 of the largest, and
+//   the sum of up to 2^14 of them is exact, so that the division's remainder is all of it.
+//   (Others differ by a quarter of the largest, so that their root is at least 2^-9 of it.)
+// * Float32 values have a sum that was rounded: what is left is summed with the squares.
+//   sum (v - m)^2 of what is left, with its mean m = sum v^2 - m sum v
 __device__ __forceinline__ float squares_around(float squares, float sum, float mean) {
   return fmaxf(fmaf(-sum, mean, squares), 0.0f);
 }
@@ -126,7 +130,8 @@ __device__ __forceinline__ float squares_around(float squares, float sum, float 
 struct Affine {
   float scale, shift;
 };
-template <bool LAYER, int TEAM, int V>
+// BF16: the values are those of a bf16 row.
+template <bool LAYER, bool BF16, int TEAM, int V>
 __device__ __forceinline__ Affine norm_of(float (&v)[V][8], const Chunks<TEAM, V>& c, float inv_cols, float eps,
                                           TeamSums<TEAM>& lds, int& turn) {
   if constexpr (LAYER) {
@@ -136,18 +141,21 @@ __device__ __forceinline__ Affine norm_of(float (&v)[V][8], const Chunks<TEAM, V
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += v[i][e];
     team_sums<TEAM>(sum, lds, turn);
-    const float mean = sum[0] / (float)(c.count * 8);
-    float s[2] = {0.0f, 0.0f};  // squares, sum of what is left
+    const float cols = (float)(c.count * 8), mean = sum[0] / cols;
+    float s[BF16 ? 1 : 2] = {};  // squares, sum of what is left
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = c.in(i) ? v[i][e] - mean : 0.0f;
-        v[i][e] = d, s[0] = fmaf(d, d, s[0]), s[1] += d;
+        v[i][e] = d, s[0] = fmaf(d, d, s[0]);
+        if constexpr (!BF16) s[1] += d;
       }
     team_sums<TEAM>(s, lds, turn);
-    const float rest = s[1] * inv_cols;
-    const float scale = inverse_root(fmaf(squares_around(s[0], s[1], rest), inv_cols, eps));
+    float left = fmaf(-mean, cols, sum[0]);
+    if constexpr (!BF16) left = s[1];
+    const float rest = left * inv_cols;
+    const float scale = inverse_root(fmaf(squares_around(s[0], left, rest), inv_cols, eps));
     return {scale, -rest * scale};
   } else {
     float squares[1] = {0.0f};
@@ -234,7 +242,7 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
 #pragma unroll
     for (int i = 0; i < V; ++i) widen8(y[i], v[i]);
     if (p.post) {
-      const Affine n = norm_of<LAYER>(v, c, inv_cols, p.eps, lds, turn);
+      const Affine n = norm_of<LAYER, true>(v, c, inv_cols, p.eps, lds, turn);
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -265,7 +273,7 @@ __global__ __launch_bounds__(kNormThreads<TEAM>) void norm_kernel(NormParams p) 
         if (c.in(i)) store8<STREAMING>(p.r + t * p.ld_r + c.at(i) * 8, v[i]);
     }
     if (!p.x && !p.q) continue;
-    const Affine norm = norm_of<LAYER>(v, c, inv_cols, p.eps, lds, turn);
+    const Affine norm = norm_of<LAYER, false>(v, c, inv_cols, p.eps, lds, turn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int at = c.at(i);
@@ -453,8 +461,8 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
       load_raw(p, t, read_y, c, raw);
     }
     // The sums that both norms' statistics need, together: the mean first (layer),
-    // then squares and products with what is left, and its own mean (squares_around).
-    float mean_r = 0.0f, mean_y = 0.0f, mean_g = 0.0f;
+    // then squares and products with what is left (of bf16 values, see squares_around).
+    float mean_r = 0.0f, mean_y = 0.0f, mean_g = 0.0f, left_r = 0.0f, left_y = 0.0f;
     if constexpr (LAYER) {
       float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -474,10 +482,11 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         }
       }
       team_sums<TEAM>(s, lds, turn);
-      mean_r = s[0] / (float)p.cols, mean_y = s[1] / (float)p.cols, mean_g = s[2] * inv_cols;
+      const float cols = (float)p.cols;
+      mean_r = s[0] / cols, mean_y = s[1] / cols, mean_g = s[2] * inv_cols;
+      left_r = fmaf(-mean_r, cols, s[0]), left_y = fmaf(-mean_y, cols, s[1]);
     }
-    // Squares of r, products of g and r, squares of y; sums of what is left of r and y.
-    float s[LAYER ? 5 : 3] = {};
+    float s[3] = {0.0f, 0.0f, 0.0f};  // squares of r, products of g and r, squares of y
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!c.in(i)) continue;
@@ -491,7 +500,6 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
           const float d = a[e] - mean_r;
           s[0] = fmaf(d, d, s[0]);
           s[1] = fmaf(b[e] * w[e], d, s[1]);
-          if constexpr (LAYER) s[3] += d;
         }
       }
       if (POST) {
@@ -500,16 +508,15 @@ __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdPara
         for (int e = 0; e < 8; ++e) {
           const float d = a[e] - mean_y;
           s[2] = fmaf(d, d, s[2]);
-          if constexpr (LAYER) s[4] += d;
         }
       }
     }
     if (p.dx || POST) team_sums<TEAM>(s, lds, turn);
     float rest_r = 0.0f, rest_y = 0.0f;
     if constexpr (LAYER) {
-      rest_r = s[3] * inv_cols, rest_y = s[4] * inv_cols;
-      s[0] = squares_around(s[0], s[3], rest_r), s[2] = squares_around(s[2], s[4], rest_y);
-      s[1] = fmaf(-mean_g, s[3], s[1]);  // rest_r times the sum of g
+      rest_r = left_r * inv_cols, rest_y = left_y * inv_cols;
+      s[0] = squares_around(s[0], left_r, rest_r), s[2] = squares_around(s[2], left_y, rest_y);
+      s[1] = fmaf(-mean_g, left_r, s[1]);  // rest_r times the sum of g
     }
     const float kr = inverse_root(fmaf(s[0], inv_cols, p.eps));
     const float ky = POST ? inverse_root(fmaf(s[2], inv_cols, p.eps)) : 1.0f;
