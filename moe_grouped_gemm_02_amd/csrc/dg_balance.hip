@@ -7,9 +7,10 @@
 // chunk, a row of sums over their common tokens: chunk b and sequence s share row
 // b + s (both only grow along the tokens, so no two pairs have the same), and a
 // second launch adds the rows of each sequence in their order.  32768 tokens of 256
-// fp32 experts: 8.5 + 6.4 us (13.4 + 6.5 with every score formed as the gradient's), and
+// fp32 experts: 8.5 + 6.6 us (13.4 + 6.5 with every score formed as the gradient's), and
 // 20 for the gradient with one to add to, 101 MB at 5 TB/s.  Of bf16 logits, half of
-// the bytes, it is bound by the vector units (172 instructions a token).
+// the bytes, 9.8 + 6.6 us and 16.2, with the vector units busy 56 and 75 % of the time:
+// their scores take the same instructions.
 
 #include "dg_block_internal.h"
 #include "dg_math.h"

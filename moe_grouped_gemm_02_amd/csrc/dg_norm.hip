@@ -340,7 +340,7 @@ __device__ __forceinline__ void load_raw(const NormBwdParams& p, int64_t t, bool
 // us, and 349 with parameters from memory).  In registers, or in shared memory, first
 // and second halves of the chunks apart, so that lanes side by side read 16 bytes side
 // by side; rows of more than 12288 values, which are not read ahead, take them from
-// memory.
+// memory (there is room for them in shared memory: not tried).
 enum ColumnsIn { kRegisters, kShared, kMemory };
 template <int TEAM, int V>
 constexpr ColumnsIn kColumnsIn = TEAM * V > 1536 ? kMemory : V == 1 ? kRegisters : kShared;
@@ -387,7 +387,9 @@ struct Columns {
 // The sums of a column gradient over a team's rows: in registers, or, where two norms
 // of rows of more than 12288 values leave none for them, each thread's in its own words
 // of shared memory (16384 columns, both norms and a column gate: 3.6 TB/s, and 1.7 with
-// sums that spill).
+// sums that spill).  With one norm they stay in registers, and with the gradient of a bias
+// or of a gate some 20 registers spill (16384 columns: 4.4 TB/s, 3.6 to 4.1 so); shared memory
+// would hold these sums too.
 template <int TEAM, int V, bool POST>
 constexpr bool kSumsInLds = POST && TEAM * V > 1536;
 template <int TEAM, int V, bool LDS>
@@ -427,10 +429,11 @@ struct ColumnAcc {
 // Gradient.  Each team walks down the rows and keeps the sums over its rows of the
 // column gradients; they leave once, as a row of partial sums of the workgroup, so that
 // the sums need no atomics and their order is fixed.  Bound by the memory: 16384 x 7168
-// with both norms 264 us, 5.4 TB/s; 4.9 to 5.5 TB/s up to 8192 columns, and above, where
-// registers run short, 3.8 to 5.3 up to 12288 and 3.1 to 4.3 up to 16384.  The next row is read while this one is worked on.  POST, LAYER: as in
-// the call; EXTRA: whether the gradients of a bias or of a column gate are wanted
-// (registers for two more sums).
+// with both norms 262 us, 5.4 TB/s; 4.9 to 5.6 TB/s up to 8192 columns (calls of a few
+// thousand short rows are two launches: 4095 x 1000 3.1 TB/s), and above, where
+// registers run short, 3.7 to 5.4 up to 12288 and 3.3 to 4.4 up to 16384.  The next row is
+// read while this one is worked on.  POST, LAYER: as in the call; EXTRA: whether the
+// gradients of a bias or of a column gate are wanted (registers for two more sums).
 template <int TEAM, int V, bool POST, bool LAYER, bool EXTRA>
 __global__ __launch_bounds__(kBwdThreads<TEAM>) void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kTeams = kBwdThreads<TEAM> / TEAM;
